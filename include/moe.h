@@ -168,6 +168,58 @@ moe_status moe_router_topk_opts(const moe_config* cfg, const void* x, const void
                                 const moe_router_opts* opts, int32_t* topk_idx, float* topk_w,
                                 void* ws, size_t ws_bytes, void* stream);
 
+/* Group-limited routing on given logits, as the "noaux_tc" router named on
+ * the page-3 model card selects (which prints no code for it): the experts lie
+ * in n_group groups of n_experts / n_group consecutive ids, a token's groups
+ * are ranked, and only the experts of the topk_group best compete.
+ * Per token with logits l:
+ *   s = sigmoid(l), or softmax over all E (cfg->gate)
+ *   key = l + sel_bias (bias_space 0) or s + sel_bias (bias_space 1)
+ *   an expert is eligible when l > -inf, s is not NaN and key > -inf
+ *   group score = its largest key (group_score 1), or the sum of its two
+ *     largest (2; of the one, where only one expert is eligible)
+ *   top_k of the chosen groups' eligible experts, descending key
+ *   w = scale s / (sum of the chosen s + 1e-9)  or  scale s
+ *     (cfg->norm_topk_prob)
+ * Equal scores or keys go to the lower id.  The selection is the one that
+ * keys in fp64 give; weights are fp32.  Where fewer than top_k experts are
+ * eligible the remaining entries are id -1, weight 0 (moe_permute skips such
+ * pairs and reports them as MOE_ERR_DATA, moe_combine adds nothing for them). */
+typedef struct {
+  int32_t n_group;       /* 1..32, divides n_experts                        */
+  int32_t topk_group;    /* 1..n_group                                      */
+  int32_t group_score;   /* 1 or 2                                          */
+  int32_t bias_space;    /* 0 or 1                                          */
+  int32_t logits_dtype;  /* moe_dtype of the logits and of their gradient   */
+  float scale;           /* factor of the weights, finite                   */
+  int32_t reserved[2];   /* 0                                               */
+} moe_group_opts;
+
+/* cfg: T, n_experts, top_k, gate and norm_topk_prob are used.
+ *   logits [T, E] of logits_dtype, rows of logits_ld elements (>= E);
+ *   sel_bias [E] fp32 or NULL (moves the selection only; -inf switches an
+ *   expert off); token_mask [T] bytes or NULL: a token with 0 (padding) gets
+ *   ids -1 and weights 0, its logits are not read.
+ *   out: topk_idx [T, k] int32, topk_w [T, k] fp32.  No workspace. */
+moe_status moe_route_groups(const moe_config* cfg, const moe_group_opts* opts,
+                            const void* logits, int64_t logits_ld, const float* sel_bias,
+                            const uint8_t* token_mask, int32_t* topk_idx, float* topk_w,
+                            void* stream);
+
+/* Gradient of <dw, topk_w> of moe_route_groups: none through the selection;
+ * with s the scores of the chosen experts, D = sum s + 1e-9,
+ *   ds_j = scale (dw_j - sum_i dw_i s_i / D) / D   or   scale dw_j
+ *   sigmoid: dl = ds s (1 - s);  softmax: dl_e = s_e (ds_e - sum_j ds_j s_j).
+ * topk_idx as moe_route_groups returned it (an entry outside [0, E) is a pair
+ * that is not there: its dw is not read; an id listed twice counts twice);
+ * dw [T, k] fp32.  out: dlogits [T, E] of logits_dtype, rows of dlogits_ld
+ * elements, every element of the E written (columns behind them are left);
+ * dlogits must not overlap the inputs. */
+moe_status moe_route_groups_backward(const moe_config* cfg, const moe_group_opts* opts,
+                                     const void* logits, int64_t logits_ld,
+                                     const int32_t* topk_idx, const float* dw, void* dlogits,
+                                     int64_t dlogits_ld, void* stream);
+
 /* Router GEMM alone: logits [T, E] fp32 = x . w_router^T (+ logit_offset),
  * for bf16 layers (fp32 layers return MOE_ERR_UNSUPPORTED).  Tensor cores,
  * exact bf16 products, fp32 accumulation: these are the logits moe_router_topk
@@ -412,6 +464,75 @@ moe_status moe_backward(const moe_config* cfg, const void* x, const void* w_rout
                         const int32_t* topk_idx, const float* topk_w, const void* dout, void* dx,
                         float* dw_router, const moe_expert_grads* g, void* fws, size_t fws_bytes,
                         void* bws, size_t bws_bytes, void* stream);
+
+/* moe_forward with the router replaced by moe_route_groups on the layer's
+ * logits (bf16 layers: the tensor cores' fp32 logits of moe_router_logits;
+ * fp32 layers: the fp64 sums of moe_router_topk's logits).  Arguments as
+ * there; groups->logits_dtype must be MOE_F32.  token_mask [T] bytes or NULL:
+ * a token with 0 (padding) goes to no expert, its out is the shared expert's
+ * row or zero; such tokens, and ones with fewer than top_k eligible experts,
+ * are not reported by moe_device_status.  offsets[E] (see
+ * moe_forward_dispatch_view) is the number of routed pairs. */
+moe_status moe_forward_grouped(const moe_config* cfg, const moe_group_opts* groups, const void* x,
+                               const void* w_router, const float* sel_bias,
+                               const float* logit_offset, const uint8_t* token_mask,
+                               const moe_expert_weights* w, void* out, int32_t* topk_idx,
+                               float* topk_w, int32_t* counts, void* ws, size_t ws_bytes,
+                               void* stream);
+
+/* moe_backward of a moe_forward_grouped call (bf16 layers): the router's part
+ * is moe_route_groups_backward's.  Arguments as moe_backward; groups as in the
+ * forward.  It may set rows of the workspace behind the routed ones to zero. */
+moe_status moe_backward_grouped(const moe_config* cfg, const moe_group_opts* groups,
+                                const void* x, const void* w_router, const float* logit_offset,
+                                const moe_expert_weights* w, const int32_t* topk_idx,
+                                const float* topk_w, const void* dout, void* dx,
+                                float* dw_router, const moe_expert_grads* g, void* fws,
+                                size_t fws_bytes, void* bws, size_t bws_bytes, void* stream);
+
+/* Orthogonalised update directions: the Newton-Schulz iteration of the Muon
+ * optimiser (the "moe-200m-qwen3-100b" README trains its matrix weights with
+ * Muon), for a batch of gradients or momenta such as moe_backward's dw1, dw3,
+ * dw2 [E, out, in] and dw_router [E, d] (batch 1).  For every matrix
+ *   X = G / (|G|_F + eps)              (its transpose when rows > cols)
+ *   steps times:  A = X X^T,  B = b A + c A A,  X = a X + B X
+ *   out = scale * X                    (transposed back)
+ * The matrices of the batch do not affect one another; a matrix of zeros
+ * gives zeros, one with a NaN or an infinity gives NaN.
+ * Precision: fp32 sums, the norm in fp64.  dtype_out MOE_F32: products of
+ * operands held to 22 bits, results within a few 1e-6 of the exact iterate
+ * (2-norm, relative).  MOE_BF16: products of operands rounded to 11 bits,
+ * results within about 1e-3 before their rounding to bf16. */
+typedef struct {
+  int32_t batch;       /* matrices, 0..65535 (0: a no-op)                     */
+  int32_t rows, cols;  /* of each, 1..65536                                   */
+  int32_t dtype_in;    /* moe_dtype of g                                      */
+  int32_t dtype_out;   /* moe_dtype of out                                    */
+  int32_t steps;       /* 1..32                                               */
+  float a, b, c;       /* the step's polynomial a x + b x^3 + c x^5; usual
+                          values 3.4445, -4.7750, 2.0315                      */
+  float eps;           /* added to the norm, at least 1e-30; usually 1e-7     */
+  float scale;         /* factor of the result                                */
+  int32_t reserved;    /* 0                                                   */
+  int64_t g_row_stride, g_batch_stride;      /* in elements; 0: dense        */
+  int64_t out_row_stride, out_batch_stride;  /* in elements; 0: dense        */
+} moe_ortho_config;
+
+/* Bytes of workspace of moe_orthogonalize (0 on an invalid configuration). */
+size_t moe_orthogonalize_workspace_size(const moe_ortho_config* cfg);
+
+/* g [batch, rows, cols] of dtype_in -> out, the same shape, of dtype_out; the
+ * elements of a row are contiguous, rows and matrices may be strided (a row
+ * stride of at least cols, a batch stride of at least the matrix; elements
+ * between the rows of out are left as they are).  out may be g itself (same
+ * type and strides); otherwise the two must not overlap.  Pointers aligned to
+ * their element.  MOE_ERR_UNSUPPORTED: a polynomial that lets singular values
+ * grow beyond sqrt(8), or |b x^2 + c x^4| beyond 8, from values in [0, 1]
+ * (the operands are kept in fp16 range by fixed scales).  ws: 256-byte
+ * aligned; its first word is a device status word read with
+ * moe_device_status(ws, ...). */
+moe_status moe_orthogonalize(const moe_ortho_config* cfg, const void* g, void* out, void* ws,
+                             size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

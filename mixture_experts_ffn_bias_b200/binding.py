@@ -62,6 +62,21 @@ class MoERouterOpts(ctypes.Structure):
                 ("sel_noise", ctypes.c_void_p)]
 
 
+class MoEGroupOpts(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("n_group", "topk_group", "group_score",
+                                               "bias_space", "logits_dtype")] +
+                [("scale", ctypes.c_float), ("reserved", ctypes.c_int32 * 2)])
+
+
+class MoEOrthoConfig(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("batch", "rows", "cols", "dtype_in", "dtype_out",
+                                               "steps")] +
+                [(n, ctypes.c_float) for n in ("a", "b", "c", "eps", "scale")] +
+                [("reserved", ctypes.c_int32)] +
+                [(n, ctypes.c_int64) for n in ("g_row_stride", "g_batch_stride",
+                                               "out_row_stride", "out_batch_stride")])
+
+
 _VP, _SZ, _I32, _F64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_double
 _CFG = ctypes.POINTER(MoEConfig)
 _WTS = ctypes.POINTER(MoEExpertWeights)
@@ -93,6 +108,17 @@ _SIGNATURES = {
     "moe_backward_workspace_size": (_SZ, [_CFG]),
     "moe_backward": (_I32, [_CFG, _VP, _VP, _VP, _WTS, _VP, _VP, _VP, _VP, _VP,
                             ctypes.POINTER(MoEExpertGrads), _VP, _SZ, _VP, _SZ, _VP]),
+    "moe_route_groups": (_I32, [_CFG, ctypes.POINTER(MoEGroupOpts), _VP, ctypes.c_int64, _VP, _VP,
+                                _VP, _VP, _VP]),
+    "moe_route_groups_backward": (_I32, [_CFG, ctypes.POINTER(MoEGroupOpts), _VP, ctypes.c_int64,
+                                         _VP, _VP, _VP, ctypes.c_int64, _VP]),
+    "moe_forward_grouped": (_I32, [_CFG, ctypes.POINTER(MoEGroupOpts), _VP, _VP, _VP, _VP, _VP,
+                                   _WTS, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "moe_backward_grouped": (_I32, [_CFG, ctypes.POINTER(MoEGroupOpts), _VP, _VP, _VP, _WTS, _VP,
+                                    _VP, _VP, _VP, _VP, ctypes.POINTER(MoEExpertGrads), _VP, _SZ,
+                                    _VP, _SZ, _VP]),
+    "moe_orthogonalize_workspace_size": (_SZ, [ctypes.POINTER(MoEOrthoConfig)]),
+    "moe_orthogonalize": (_I32, [ctypes.POINTER(MoEOrthoConfig), _VP, _VP, _VP, _SZ, _VP]),
 }
 
 _lib = None
@@ -313,6 +339,107 @@ def moe_backward(cfg, x, w_router, logit_offset, weights: Dict, topk_idx, topk_w
                             ctypes.byref(w), _p(topk_idx), _p(topk_w), _p(dout), _p(dx),
                             _p(dw_router), ctypes.byref(g), _p(fws), _nbytes(fws), _p(bws),
                             _nbytes(bws), _s(stream))
+    return _check(st, check)
+
+
+def make_group_opts(n_group=1, topk_group=1, group_score=2, bias_space=1, scale=1.0,
+                    logits_dtype=DTYPE_F32) -> MoEGroupOpts:
+    """Options of moe_route_groups: n_group groups of consecutive experts, the
+    topk_group best of which a token uses."""
+    return MoEGroupOpts(n_group, topk_group, group_score, bias_space, logits_dtype, scale)
+
+
+def _logits_ld(t, cfg, what="logits") -> int:
+    """Row stride of a [T, E] tensor whose rows are contiguous."""
+    if tuple(t.shape) != (cfg.T, cfg.n_experts):
+        raise MoEError(MOE_ERR_INVALID,
+                       f"{what} of shape {tuple(t.shape)}, expected {(cfg.T, cfg.n_experts)}")
+    if t.stride(1) != 1 and cfg.n_experts > 1:
+        raise MoEError(MOE_ERR_INVALID, f"the elements of a row of {what} must be contiguous")
+    return t.stride(0) if cfg.T > 1 else cfg.n_experts
+
+
+def moe_route_groups(cfg, opts, logits, sel_bias, token_mask, topk_idx, topk_w, stream=None,
+                     check=True) -> int:
+    """Group-limited routing of logits [T, E] (rows may be strided); token_mask
+    [T] uint8 or bool, 0 for padding, or None."""
+    st = lib().moe_route_groups(ctypes.byref(cfg), ctypes.byref(opts), _p(logits),
+                                _logits_ld(logits, cfg), _p(sel_bias), _p(token_mask),
+                                _p(topk_idx), _p(topk_w), _s(stream))
+    return _check(st, check)
+
+
+def moe_route_groups_backward(cfg, opts, logits, topk_idx, dw, dlogits, stream=None,
+                              check=True) -> int:
+    """dlogits [T, E] of <dw, topk_w> of moe_route_groups."""
+    st = lib().moe_route_groups_backward(ctypes.byref(cfg), ctypes.byref(opts), _p(logits),
+                                         _logits_ld(logits, cfg), _p(topk_idx), _p(dw),
+                                         _p(dlogits), _logits_ld(dlogits, cfg, "dlogits"),
+                                         _s(stream))
+    return _check(st, check)
+
+
+def moe_forward_grouped(cfg, groups, x, w_router, sel_bias, logit_offset, token_mask,
+                        weights: Dict, out, topk_idx, topk_w, counts, ws, stream=None,
+                        check=True) -> int:
+    """moe_forward routed by moe_route_groups (groups: MoEGroupOpts)."""
+    w = expert_weights(weights)
+    st = lib().moe_forward_grouped(ctypes.byref(cfg), ctypes.byref(groups), _p(x), _p(w_router),
+                                   _p(sel_bias), _p(logit_offset), _p(token_mask),
+                                   ctypes.byref(w), _p(out), _p(topk_idx), _p(topk_w),
+                                   _p(counts), _p(ws), _nbytes(ws) if ws is not None else 0,
+                                   _s(stream))
+    return _check(st, check)
+
+
+def moe_backward_grouped(cfg, groups, x, w_router, logit_offset, weights: Dict, topk_idx, topk_w,
+                         dout, dx, dw_router, grads: Dict, fws, bws, stream=None,
+                         check=True) -> int:
+    """Backward of a moe_forward_grouped call; the rest as moe_backward."""
+    w = expert_weights(weights)
+    g = MoEExpertGrads(*[_p(grads.get(n)) for n in ("dw1", "dw3", "dw2", "dws1", "dws3",
+                                                      "dws2")])
+    st = lib().moe_backward_grouped(ctypes.byref(cfg), ctypes.byref(groups), _p(x), _p(w_router),
+                                    _p(logit_offset), ctypes.byref(w), _p(topk_idx), _p(topk_w),
+                                    _p(dout), _p(dx), _p(dw_router), ctypes.byref(g), _p(fws),
+                                    _nbytes(fws), _p(bws), _nbytes(bws), _s(stream))
+    return _check(st, check)
+
+
+MUON_COEFFS = (3.4445, -4.7750, 2.0315)
+
+
+def make_ortho_config(batch, rows, cols, in_dtype=DTYPE_BF16, out_dtype=DTYPE_BF16, steps=5,
+                      coeffs=MUON_COEFFS, eps=1e-7, scale=1.0) -> MoEOrthoConfig:
+    """Configuration of moe_orthogonalize (dense strides; the call itself fills
+    in the strides of the tensors it is given)."""
+    return MoEOrthoConfig(batch, rows, cols, in_dtype, out_dtype, steps, *coeffs, eps, scale)
+
+
+def moe_orthogonalize_workspace_size(cfg: MoEOrthoConfig) -> int:
+    return int(lib().moe_orthogonalize_workspace_size(ctypes.byref(cfg)))
+
+
+def _matrix_strides(t, cfg):
+    """(row, batch) stride of a [batch, rows, cols] (or [rows, cols]) tensor
+    whose rows are contiguous; 0 where a dimension has one entry."""
+    want = (cfg.batch, cfg.rows, cfg.cols)
+    if tuple(t.shape) != want and not (cfg.batch == 1 and tuple(t.shape) == want[1:]):
+        raise MoEError(MOE_ERR_INVALID, f"tensor of shape {tuple(t.shape)}, expected {want}")
+    row, col = t.stride()[-2:]
+    if col != 1 and cfg.cols > 1:
+        raise MoEError(MOE_ERR_INVALID, "the elements of a matrix row must be contiguous")
+    return (row if cfg.rows > 1 else 0), (t.stride(0) if cfg.batch > 1 else 0)
+
+
+def moe_orthogonalize(cfg, g, out, ws, stream=None, check=True) -> int:
+    """Newton-Schulz orthogonalisation of g [batch, rows, cols] into out; the
+    tensors' own row and batch strides are used."""
+    c = MoEOrthoConfig.from_buffer_copy(cfg)
+    c.g_row_stride, c.g_batch_stride = _matrix_strides(g, cfg)
+    c.out_row_stride, c.out_batch_stride = _matrix_strides(out, cfg)
+    st = lib().moe_orthogonalize(ctypes.byref(c), _p(g), _p(out), _p(ws),
+                                 _nbytes(ws) if ws is not None else 0, _s(stream))
     return _check(st, check)
 
 

@@ -89,12 +89,13 @@ dispatch_rank_kernel(const int32_t* __restrict__ topk_idx, int T, int k, int E,
 // below), then puts the ticket counter back to zero.  done: zero at launch.
 // fold_cnt (or null): the folded combine's per-(token, column tile) counts,
 // set to the number of the token's skipped pairs (rows that never arrive).
+// allow_none: id -1 is "no expert" and not reported.
 __global__ void __launch_bounds__(kRankBlock)
 dispatch_rank_scan_kernel(const int32_t* __restrict__ topk_idx, int T, int k, int E,
                           int32_t* __restrict__ blk, int32_t* __restrict__ rank_out,
                           int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
                           uint32_t* __restrict__ status, uint32_t* __restrict__ done,
-                          int32_t* __restrict__ fold_cnt, int fold_nt) {
+                          int32_t* __restrict__ fold_cnt, int fold_nt, bool allow_none) {
   pdl_trigger();
   pdl_wait();
   __shared__ uint32_t masks[kMaxE][kWords];
@@ -111,7 +112,7 @@ dispatch_rank_scan_kernel(const int32_t* __restrict__ topk_idx, int T, int k, in
       if (pair_valid(row, j, E))
         atomicOr(&masks[row[j]][word], 1u << lane);
       else
-        bad = true;
+        bad = bad || !(allow_none && row[j] == -1);
     }
   }
   __syncthreads();
@@ -327,11 +328,11 @@ cudaError_t dispatch_rank(const int32_t* topk_idx, int T, int k, int E, int32_t*
 cudaError_t dispatch_rank_scan(const int32_t* topk_idx, int T, int k, int E, int32_t* blk,
                                int32_t* rank_out, int32_t* counts, int32_t* offsets,
                                uint32_t* status, uint32_t* done, cudaStream_t stream,
-                               int32_t* fold_cnt, int fold_nt) {
+                               int32_t* fold_cnt, int fold_nt, bool allow_none) {
   if (E > kMaxE || kRankBlock != kMaxE) return cudaErrorInvalidValue;
   return launch_pdl(dispatch_rank_scan_kernel, dim3(rank_blocks(T)), dim3(kRankBlock), 0, stream,
                     topk_idx, T, k, E, blk, rank_out, counts, offsets, status, done, fold_cnt,
-                    fold_nt);
+                    fold_nt, allow_none);
 }
 
 cudaError_t dispatch_scan(int32_t* blk_counts, int nblk, int E, int32_t* counts,

@@ -61,6 +61,27 @@ cudaError_t router_refine(const void* x, const void* w_router, const float* logi
                           const int32_t* refine_list, const int32_t* refine_cand,
                           int32_t* topk_idx, float* topk_w, int sms, cudaStream_t stream);
 
+// Group-limited routing on given logits (route_groups.cu): rows of ld
+// elements.  mask [T] bytes (0: the token gets no experts) or null.
+struct RouteShape {
+  int T, E, k, groups, topk_group, group_score, gate, space, norm;
+  float scale;
+  long long ld;
+};
+enum class RouteLogits { f32, bf16, f64 };   // f64: forward only
+cudaError_t route_groups(const RouteShape& a, RouteLogits type, const void* logits,
+                         const float* bias, const uint8_t* mask, int32_t* topk_idx,
+                         float* topk_w, cudaStream_t stream);
+// dlogits (the logits' type, rows of dld elements) from dw [T, k].
+cudaError_t route_groups_backward(const RouteShape& a, RouteLogits type, const void* logits,
+                                  const int32_t* topk_idx, const float* dw, void* dlogits,
+                                  long long dld, cudaStream_t stream);
+
+// Rows [offsets[E], offsets[E] + 64) of a [R, a_cols] and b [R, b_cols] (bf16,
+// columns a multiple of 8) set to zero.
+cudaError_t zero_tail_rows(const int32_t* offsets, int E, long long R, void* a, int a_cols,
+                           void* b, int b_cols, cudaStream_t stream);
+
 // logits[t, e] += offset[e]
 cudaError_t add_row_offset(float* logits, const float* offset, int T, int E, cudaStream_t stream);
 
@@ -79,11 +100,13 @@ cudaError_t dispatch_rank(const int32_t* topk_idx, int T, int k, int E, int32_t*
 // dispatch_rank followed by dispatch_scan in one launch (the last block to
 // finish scans); done: a zeroed counter, zero again when the kernel ends.
 // fold_cnt [T, fold_nt] (or null) is set to each token's skipped pairs, the
-// starting counts of the combine folded into the down pass.
+// starting counts of the combine folded into the down pass.  allow_none: a
+// pair of id -1 is skipped without being reported.
 cudaError_t dispatch_rank_scan(const int32_t* topk_idx, int T, int k, int E, int32_t* blk,
                                int32_t* rank_out, int32_t* counts, int32_t* offsets,
                                uint32_t* status, uint32_t* done, cudaStream_t stream,
-                               int32_t* fold_cnt = nullptr, int fold_nt = 0);
+                               int32_t* fold_cnt = nullptr, int fold_nt = 0,
+                               bool allow_none = false);
 cudaError_t dispatch_scan(int32_t* blk_counts, int nblk, int E, int32_t* counts,
                           int32_t* offsets, cudaStream_t stream);
 // slot_pos (in: rank inside its block of blk_tokens tokens, out: row) and
@@ -207,6 +230,22 @@ cudaError_t router_grad_split(const float* dlogits, int T, int E, const RouterGr
 // out [E, d] fp32 = sum over slices and terms of part [G, 3 Ep, d].
 cudaError_t router_grad_reduce(const float* part, const RouterGradShape& r, int E, int d,
                                float* out, cudaStream_t stream);
+
+// Orthogonalisation -----------------------------------------------------------
+// out = scale * (Newton-Schulz iterate of G / (|G|_F + eps)), see
+// orthogonalize_sm100.cu.  Row strides (ld) and matrix strides (bs) in
+// elements; status: the first word of ws, cleared by the call.
+struct OrthoShape {
+  int batch, rows, cols;
+  int in_bf16, out_bf16;     // else fp32
+  int steps;
+  float a, b, c, eps, scale;
+  long long g_ld, g_bs, out_ld, out_bs;
+};
+size_t ortho_workspace(const OrthoShape& s);
+bool ortho_coeffs_ok(float a, float b, float c, int steps);
+cudaError_t orthogonalize(const OrthoShape& s, const void* g, void* out, void* ws,
+                          cudaStream_t stream);
 
 // Combine / bias ---------------------------------------------------------------
 cudaError_t combine(bool bf16, const void* y_perm, const int32_t* slot_pos, const float* topk_w,

@@ -2,6 +2,7 @@
 // validation, workspace layout and the launch sequence of each call.
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstddef>
 #include <cstdint>
 
@@ -149,17 +150,18 @@ moe_status run_router(const moe_config* c, const void* x, const void* w_router,
 
 // fold_nt > 0: also set the folded combine's counts ([T, fold_nt] in ws).
 // copy_counters (x_perm == nullptr only): also zero the counters of a gate/up
-// launch that copies its own rows.
+// launch that copies its own rows.  allow_none: id -1 is not reported.
 moe_status run_permute(const moe_config* c, const int32_t* topk_idx, const void* x,
                        int32_t* counts, int32_t* offsets, int32_t* slot_pos, int32_t* perm_src,
                        void* x_perm, void* ws, cudaStream_t s, int fold_nt = 0,
-                       bool copy_counters = false) {
+                       bool copy_counters = false, bool allow_none = false) {
   const Layout L = layout(*c);
   int32_t* blk = at<int32_t>(ws, L.blk);
   uint32_t* status = at<uint32_t>(ws, L.status);
   MOE_TRY(moe::dispatch_rank_scan(topk_idx, c->T, c->top_k, c->n_experts, blk, slot_pos, counts,
                                   offsets, status, status + 3, s,
-                                  fold_nt > 0 ? at<int32_t>(ws, L.fold) : nullptr, fold_nt));
+                                  fold_nt > 0 ? at<int32_t>(ws, L.fold) : nullptr, fold_nt,
+                                  allow_none));
   if (x_perm == nullptr) {   // rows only; the experts gather x through perm_src
     const int n_zero =
         copy_counters ? 1 + static_cast<int>((static_cast<int64_t>(c->T) * c->top_k + 31) / 32)
@@ -253,13 +255,70 @@ moe_status check_weights(const moe_config* c, const moe_expert_weights* w) {
   return MOE_OK;
 }
 
+// cfg and opts of a group-limited routing call -> the launcher's shape.
+moe_status route_shape(const moe_config* c, const moe_group_opts* o, int64_t ld,
+                       moe::RouteShape* s) {
+  const moe_status st = check_cfg(c);
+  if (st != MOE_OK) return st;
+  if (o == nullptr || o->n_group < 1 || o->topk_group < 1 || o->topk_group > o->n_group ||
+      c->n_experts % o->n_group != 0 || (o->group_score != 1 && o->group_score != 2) ||
+      (o->bias_space != 0 && o->bias_space != 1) ||
+      (o->logits_dtype != MOE_F32 && o->logits_dtype != MOE_BF16) || !std::isfinite(o->scale) ||
+      o->reserved[0] != 0 || o->reserved[1] != 0)
+    return MOE_ERR_INVALID;
+  if (o->n_group > 32) return MOE_ERR_UNSUPPORTED;
+  if (ld < c->n_experts || ld > (int64_t{1} << 31)) return MOE_ERR_INVALID;
+  *s = moe::RouteShape{c->T,    c->n_experts,  c->top_k,          o->n_group,
+                       o->topk_group, o->group_score, c->gate, o->bias_space,
+                       c->norm_topk_prob, o->scale, ld};
+  return MOE_OK;
+}
+
+inline bool logits_aligned(const void* p, int32_t dtype) {
+  return (reinterpret_cast<uintptr_t>(p) & (dtype == MOE_BF16 ? 1u : 3u)) == 0;
+}
+
+inline moe::RouteLogits logits_type(int32_t dtype) {
+  return dtype == MOE_BF16 ? moe::RouteLogits::bf16 : moe::RouteLogits::f32;
+}
+
+// Group-limited router of the layer calls: the layer's logits (fp32 from the
+// tensor cores, fp64 for fp32 layers) in ws, then the selection on them.
+moe_status run_router_grouped(const moe_config* c, const moe::RouteShape& rs, const void* x,
+                              const void* w_router, const float* sel_bias,
+                              const float* logit_offset, const uint8_t* token_mask,
+                              int32_t* topk_idx, float* topk_w, void* ws, cudaStream_t s) {
+  const Layout L = layout(*c);
+  void* logits = at<void>(ws, L.logits);
+  if (c->dtype == MOE_BF16) {
+    float* lf = static_cast<float*>(logits);
+    MOE_TRY(moe::router_logits_tc(x, c->T, w_router, c->n_experts, c->d_model, lf,
+                                  at<uint32_t>(ws, L.status), s));
+    if (logit_offset) MOE_TRY(moe::add_row_offset(lf, logit_offset, c->T, c->n_experts, s));
+  } else {
+    MOE_TRY(moe::router_logits(false, x, w_router, logit_offset, c->T, c->d_model, c->n_experts,
+                               static_cast<double*>(logits), s));
+  }
+  MOE_TRY(moe::route_groups(rs, c->dtype == MOE_BF16 ? moe::RouteLogits::f32
+                                                     : moe::RouteLogits::f64,
+                            logits, sel_bias, token_mask, topk_idx, topk_w, s));
+  return MOE_OK;
+}
+
 moe_status forward_impl(const moe_config* cfg, const void* x, const void* w_router,
                         const float* sel_bias, const float* logit_offset,
                         const moe_expert_weights* w, void* out, int32_t* topk_idx,
                         float* topk_w, int32_t* counts, void* ws, size_t ws_bytes, void* stream,
-                        void* const* events, const moe_forward_opts* opts = nullptr) {
+                        void* const* events, const moe_forward_opts* opts = nullptr,
+                        const moe_group_opts* groups = nullptr,
+                        const uint8_t* token_mask = nullptr) {
   moe_status st = check_cfg(cfg);
   if (st != MOE_OK) return st;
+  moe::RouteShape rs{};
+  if (groups != nullptr) {
+    if ((st = route_shape(cfg, groups, cfg->n_experts, &rs)) != MOE_OK) return st;
+    if (groups->logits_dtype != MOE_F32) return MOE_ERR_INVALID;
+  }
   if (opts != nullptr &&
       ((opts->gather_rows != 0 && opts->gather_rows != 1) ||
        (opts->fold_combine != 0 && opts->fold_combine != 1) ||
@@ -290,9 +349,11 @@ moe_status forward_impl(const moe_config* cfg, const void* x, const void* w_rout
   const Marks mk{events, s};
   if ((st = clear_status(ws, s)) != MOE_OK) return st;
   if (!mk.rec(0)) return MOE_ERR_CUDA;
-  if ((st = run_router(cfg, x, w_router, sel_bias, logit_offset, topk_idx, topk_w, ws, s)) !=
-      MOE_OK)
-    return st;
+  st = groups != nullptr
+           ? run_router_grouped(cfg, rs, x, w_router, sel_bias, logit_offset, token_mask, topk_idx,
+                                topk_w, ws, s)
+           : run_router(cfg, x, w_router, sel_bias, logit_offset, topk_idx, topk_w, ws, s);
+  if (st != MOE_OK) return st;
   if (!mk.rec(1)) return MOE_ERR_CUDA;
   int32_t* offsets = at<int32_t>(ws, L.offsets);
   int32_t* slot_pos = at<int32_t>(ws, L.slot_pos);
@@ -315,7 +376,8 @@ moe_status forward_impl(const moe_config* cfg, const void* x, const void* w_rout
   // scatter_in_gemm: dispatch writes the rows' positions only, and the
   // gate/up GEMM copies x's rows into x_perm while it runs
   if ((st = run_permute(cfg, topk_idx, x, counts, offsets, slot_pos, perm_src,
-                        (gather || scat) ? nullptr : x_perm, ws, s, fold_nt, scat)) != MOE_OK)
+                        (gather || scat) ? nullptr : x_perm, ws, s, fold_nt, scat,
+                        groups != nullptr)) != MOE_OK)
     return st;
   if (!mk.rec(2)) return MOE_ERR_CUDA;
   const moe::GemmFold gf{at<int32_t>(ws, L.fold), fold_nt, cfg->T, cfg->top_k, perm_src,
@@ -373,7 +435,7 @@ moe_status backward_impl(const moe_config* c, const void* x, const void* w_route
                          const float* logit_offset, const moe_expert_weights* w,
                          const int32_t* topk_idx, const float* topk_w, const void* dout,
                          void* dx, float* dw_router, const moe_expert_grads* g, void* fws,
-                         void* bws, cudaStream_t s) {
+                         void* bws, cudaStream_t s, const moe::RouteShape* groups = nullptr) {
   const Layout L = layout(*c);
   const BLayout B = blayout(*c);
   const int T = c->T, d = c->d_model, E = c->n_experts, F = c->d_ff, k = c->top_k;
@@ -397,6 +459,8 @@ moe_status backward_impl(const moe_config* c, const void* x, const void* w_route
   // SwiGLU backward runs in that GEMM's epilogue: [dG | dU] from G, U, dH.
   void* x_perm = at<void>(fws, L.x_perm);
   MOE_TRY(moe::fill_xperm(x, perm_src, at<uint32_t>(fws, L.status) + 2, x_perm, R, T, d, s));
+  if (groups != nullptr)
+    MOE_TRY(moe::zero_tail_rows(offsets, E, R, x_perm, d, at<void>(fws, L.h), F, s));
   MOE_TRY(moe::grouped_swiglu_bwd_bf16(x_perm, R, offsets, E, 0, w->w1, w->w3, F, d,
                                        at<void>(bws, B.dh), at<void>(bws, B.dgu), status, s));
   MOE_TRY(moe::grouped_gemm_bmn_bf16(at<void>(bws, B.dgu), R, offsets, E, 0, w->w1, w->w3, F, d,
@@ -435,8 +499,14 @@ moe_status backward_impl(const moe_config* c, const void* x, const void* w_route
   float* logits = at<float>(bws, B.logits);
   float* dlogits = at<float>(bws, B.dlogits);
   MOE_TRY(moe::router_logits_tc(x, T, w_router, E, d, logits, status, s));
-  MOE_TRY(moe::router_dlogits(logits, logit_offset, topk_idx, topk_w, dw, T, E, k, c->gate,
-                              c->norm_topk_prob, dlogits, s));
+  if (groups != nullptr) {
+    if (logit_offset) MOE_TRY(moe::add_row_offset(logits, logit_offset, T, E, s));
+    MOE_TRY(moe::route_groups_backward(*groups, moe::RouteLogits::f32, logits, topk_idx, dw,
+                                       dlogits, E, s));
+  } else {
+    MOE_TRY(moe::router_dlogits(logits, logit_offset, topk_idx, topk_w, dw, T, E, k, c->gate,
+                                c->norm_topk_prob, dlogits, s));
+  }
   const moe::RouterGradShape rg = moe::router_grad_shape(T, E);
   const int C3 = 3 * rg.Ep;
   uint8_t* wr3 = at<uint8_t>(bws, B.wr3);
@@ -457,6 +527,81 @@ moe_status backward_impl(const moe_config* c, const void* x, const void* w_route
   MOE_TRY(moe::router_grad_reduce(at<float>(bws, B.pdw), rg, E, d, dw_router, s));
   MOE_TRY(moe::dx_gather(at<void>(bws, B.dxp), slot_pos, at<float>(bws, B.dxr), dxs, dx, T, d, k,
                          s));
+  return MOE_OK;
+}
+
+// moe_backward / moe_backward_grouped (groups not null).
+moe_status backward_checked(const moe_config* cfg, const moe_group_opts* groups, const void* x,
+                            const void* w_router, const float* logit_offset,
+                            const moe_expert_weights* w, const int32_t* topk_idx,
+                            const float* topk_w, const void* dout, void* dx, float* dw_router,
+                            const moe_expert_grads* g, void* fws, size_t fws_bytes, void* bws,
+                            size_t bws_bytes, void* stream) {
+  moe_status st = check_cfg(cfg);
+  if (st != MOE_OK) return st;
+  moe::RouteShape rs{};
+  if (groups != nullptr) {
+    if ((st = route_shape(cfg, groups, cfg->n_experts, &rs)) != MOE_OK) return st;
+    if (groups->logits_dtype != MOE_F32) return MOE_ERR_INVALID;
+  }
+  if (cfg->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (cfg->T == 0) return MOE_OK;
+  if (!x || !w_router || !topk_idx || !topk_w || !dout || !dx || !dw_router || !g || !g->dw1 ||
+      !g->dw3 || !g->dw2 || (cfg->n_shared && (!g->dws1 || !g->dws3 || !g->dws2)))
+    return MOE_ERR_INVALID;
+  if ((st = check_weights(cfg, w)) != MOE_OK) return st;
+  if (!aligned16(x) || !aligned16(w_router) || !aligned16(dout) || !aligned16(dx) ||
+      !aligned16(dw_router) || !aligned4(topk_idx) || !aligned4(topk_w) || !aligned16(g->dw1) ||
+      !aligned16(g->dw3) || !aligned16(g->dw2) || (logit_offset && !aligned4(logit_offset)) ||
+      (cfg->n_shared && (!aligned16(g->dws1) || !aligned16(g->dws3) || !aligned16(g->dws2))))
+    return MOE_ERR_INVALID;
+  if ((st = check_ws(cfg, fws, fws_bytes)) != MOE_OK) return st;
+  if (bws == nullptr || (reinterpret_cast<uintptr_t>(bws) & (kAlign - 1))) return MOE_ERR_INVALID;
+  if (bws_bytes < blayout(*cfg).total) return MOE_ERR_WORKSPACE;
+  cudaStream_t s = S(stream);
+  if ((st = clear_status(bws, s)) != MOE_OK) return st;
+  return backward_impl(cfg, x, w_router, logit_offset, w, topk_idx, topk_w, dout, dx, dw_router,
+                       g, fws, bws, s, groups != nullptr ? &rs : nullptr);
+}
+
+// moe_ortho_config -> the launcher's shape, dense strides filled in.
+moe_status ortho_shape(const moe_ortho_config* c, moe::OrthoShape* s) {
+  if (c == nullptr) return MOE_ERR_INVALID;
+  if (c->batch < 0 || c->rows < 1 || c->cols < 1 || c->steps < 1 || c->reserved != 0)
+    return MOE_ERR_INVALID;
+  if ((c->dtype_in != MOE_F32 && c->dtype_in != MOE_BF16) ||
+      (c->dtype_out != MOE_F32 && c->dtype_out != MOE_BF16))
+    return MOE_ERR_INVALID;
+  if (!std::isfinite(c->a) || !std::isfinite(c->b) || !std::isfinite(c->c) ||
+      !std::isfinite(c->scale) || !std::isfinite(c->eps) || !(c->eps >= 1e-30f))
+    return MOE_ERR_INVALID;
+  if (c->batch > 65535 || c->rows > 65536 || c->cols > 65536 || c->steps > 32)
+    return MOE_ERR_UNSUPPORTED;
+  s->batch = c->batch;
+  s->rows = c->rows;
+  s->cols = c->cols;
+  s->in_bf16 = c->dtype_in == MOE_BF16;
+  s->out_bf16 = c->dtype_out == MOE_BF16;
+  s->steps = c->steps;
+  s->a = c->a;
+  s->b = c->b;
+  s->c = c->c;
+  s->eps = c->eps;
+  s->scale = c->scale;
+  const int64_t strides[4] = {c->g_row_stride, c->g_batch_stride, c->out_row_stride,
+                              c->out_batch_stride};
+  long long* dst[4] = {&s->g_ld, &s->g_bs, &s->out_ld, &s->out_bs};
+  constexpr int64_t kMax = int64_t{1} << 46;   // byte offsets stay far inside 64 bits
+  for (int i = 0; i < 4; i += 2) {
+    const int64_t ld = strides[i] == 0 ? c->cols : strides[i];
+    if (ld < c->cols || ld > kMax) return MOE_ERR_INVALID;
+    const int64_t need = ld * (c->rows - 1) + c->cols;
+    const int64_t bs = strides[i + 1] == 0 ? ld * c->rows : strides[i + 1];
+    if (bs < need || bs > kMax) return MOE_ERR_INVALID;
+    *dst[i] = ld;
+    *dst[i + 1] = bs;
+  }
+  if (!moe::ortho_coeffs_ok(c->a, c->b, c->c, c->steps)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -716,26 +861,84 @@ moe_status moe_backward(const moe_config* cfg, const void* x, const void* w_rout
                         const int32_t* topk_idx, const float* topk_w, const void* dout, void* dx,
                         float* dw_router, const moe_expert_grads* g, void* fws, size_t fws_bytes,
                         void* bws, size_t bws_bytes, void* stream) {
-  moe_status st = check_cfg(cfg);
+  return backward_checked(cfg, nullptr, x, w_router, logit_offset, w, topk_idx, topk_w, dout, dx,
+                          dw_router, g, fws, fws_bytes, bws, bws_bytes, stream);
+}
+
+moe_status moe_forward_grouped(const moe_config* cfg, const moe_group_opts* groups, const void* x,
+                               const void* w_router, const float* sel_bias,
+                               const float* logit_offset, const uint8_t* token_mask,
+                               const moe_expert_weights* w, void* out, int32_t* topk_idx,
+                               float* topk_w, int32_t* counts, void* ws, size_t ws_bytes,
+                               void* stream) {
+  if (groups == nullptr) return MOE_ERR_INVALID;
+  return forward_impl(cfg, x, w_router, sel_bias, logit_offset, w, out, topk_idx, topk_w, counts,
+                      ws, ws_bytes, stream, nullptr, nullptr, groups, token_mask);
+}
+
+moe_status moe_backward_grouped(const moe_config* cfg, const moe_group_opts* groups,
+                                const void* x, const void* w_router, const float* logit_offset,
+                                const moe_expert_weights* w, const int32_t* topk_idx,
+                                const float* topk_w, const void* dout, void* dx,
+                                float* dw_router, const moe_expert_grads* g, void* fws,
+                                size_t fws_bytes, void* bws, size_t bws_bytes, void* stream) {
+  if (groups == nullptr) return MOE_ERR_INVALID;
+  return backward_checked(cfg, groups, x, w_router, logit_offset, w, topk_idx, topk_w, dout, dx,
+                          dw_router, g, fws, fws_bytes, bws, bws_bytes, stream);
+}
+
+moe_status moe_route_groups(const moe_config* cfg, const moe_group_opts* opts,
+                            const void* logits, int64_t logits_ld, const float* sel_bias,
+                            const uint8_t* token_mask, int32_t* topk_idx, float* topk_w,
+                            void* stream) {
+  moe::RouteShape s;
+  const moe_status st = route_shape(cfg, opts, logits_ld, &s);
   if (st != MOE_OK) return st;
-  if (cfg->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
   if (cfg->T == 0) return MOE_OK;
-  if (!x || !w_router || !topk_idx || !topk_w || !dout || !dx || !dw_router || !g || !g->dw1 ||
-      !g->dw3 || !g->dw2 || (cfg->n_shared && (!g->dws1 || !g->dws3 || !g->dws2)))
+  if (!logits || !topk_idx || !topk_w || !logits_aligned(logits, opts->logits_dtype) ||
+      !aligned4(topk_idx) || !aligned4(topk_w) || (sel_bias && !aligned4(sel_bias)))
     return MOE_ERR_INVALID;
-  if ((st = check_weights(cfg, w)) != MOE_OK) return st;
-  if (!aligned16(x) || !aligned16(w_router) || !aligned16(dout) || !aligned16(dx) ||
-      !aligned16(dw_router) || !aligned4(topk_idx) || !aligned4(topk_w) || !aligned16(g->dw1) ||
-      !aligned16(g->dw3) || !aligned16(g->dw2) || (logit_offset && !aligned4(logit_offset)) ||
-      (cfg->n_shared && (!aligned16(g->dws1) || !aligned16(g->dws3) || !aligned16(g->dws2))))
+  MOE_TRY(moe::route_groups(s, logits_type(opts->logits_dtype), logits, sel_bias, token_mask,
+                            topk_idx, topk_w, S(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_route_groups_backward(const moe_config* cfg, const moe_group_opts* opts,
+                                     const void* logits, int64_t logits_ld,
+                                     const int32_t* topk_idx, const float* dw, void* dlogits,
+                                     int64_t dlogits_ld, void* stream) {
+  moe::RouteShape s;
+  const moe_status st = route_shape(cfg, opts, logits_ld, &s);
+  if (st != MOE_OK) return st;
+  if (dlogits_ld < cfg->n_experts || dlogits_ld > (int64_t{1} << 31)) return MOE_ERR_INVALID;
+  if (cfg->T == 0) return MOE_OK;
+  if (!logits || !topk_idx || !dw || !dlogits || !logits_aligned(logits, opts->logits_dtype) ||
+      !logits_aligned(dlogits, opts->logits_dtype) || !aligned4(topk_idx) || !aligned4(dw))
     return MOE_ERR_INVALID;
-  if ((st = check_ws(cfg, fws, fws_bytes)) != MOE_OK) return st;
-  if (bws == nullptr || (reinterpret_cast<uintptr_t>(bws) & (kAlign - 1))) return MOE_ERR_INVALID;
-  if (bws_bytes < blayout(*cfg).total) return MOE_ERR_WORKSPACE;
-  cudaStream_t s = S(stream);
-  if ((st = clear_status(bws, s)) != MOE_OK) return st;
-  return backward_impl(cfg, x, w_router, logit_offset, w, topk_idx, topk_w, dout, dx, dw_router,
-                       g, fws, bws, s);
+  MOE_TRY(moe::route_groups_backward(s, logits_type(opts->logits_dtype), logits, topk_idx, dw,
+                                     dlogits, dlogits_ld, S(stream)));
+  return MOE_OK;
+}
+
+size_t moe_orthogonalize_workspace_size(const moe_ortho_config* cfg) {
+  moe::OrthoShape s;
+  if (ortho_shape(cfg, &s) != MOE_OK) return 0;
+  return moe::ortho_workspace(s);
+}
+
+moe_status moe_orthogonalize(const moe_ortho_config* cfg, const void* g, void* out, void* ws,
+                             size_t ws_bytes, void* stream) {
+  moe::OrthoShape s;
+  const moe_status st = ortho_shape(cfg, &s);
+  if (st != MOE_OK) return st;
+  if (s.batch == 0) return MOE_OK;
+  if (!g || !out || (reinterpret_cast<uintptr_t>(g) & (s.in_bf16 ? 1u : 3u)) ||
+      (reinterpret_cast<uintptr_t>(out) & (s.out_bf16 ? 1u : 3u)))
+    return MOE_ERR_INVALID;
+  if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1))) return MOE_ERR_INVALID;
+  if (ws_bytes < moe::ortho_workspace(s)) return MOE_ERR_WORKSPACE;
+  MOE_TRY(moe::orthogonalize(s, g, out, ws, S(stream)));
+  return MOE_OK;
 }
 
 const char* moe_status_string(moe_status s) {

@@ -29,8 +29,11 @@ def to_device(a: np.ndarray, dtype: torch.dtype, device) -> torch.Tensor:
 
 
 class MoELayer:
-    def __init__(self, shape: MoEShape, host: Dict[str, np.ndarray], device="cuda"):
+    def __init__(self, shape: MoEShape, host: Dict[str, np.ndarray], device="cuda",
+                 groups: Optional[B.MoEGroupOpts] = None):
+        """groups (binding.make_group_opts): route with moe_route_groups."""
         self.shape = shape
+        self.groups = groups
         self.device = torch.device(device)
         self.cfg = B.config_from_shape(shape)
         st = B.moe_check_config(self.cfg)
@@ -56,9 +59,23 @@ class MoELayer:
     # ----------------------------------------------------------------- calls
     def forward(self, x: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
                 stream=None, gather_rows: bool = False, fold_combine: bool = False,
-                scatter_in_gemm: bool = False) -> torch.Tensor:
+                scatter_in_gemm: bool = False,
+                token_mask: Optional[torch.Tensor] = None) -> torch.Tensor:
         """The layer forward (moe_forward; moe_forward_ex with gather_rows,
-        fold_combine or scatter_in_gemm)."""
+        fold_combine or scatter_in_gemm; moe_forward_grouped for a layer with
+        groups, which also takes a token_mask [T] uint8 or bool, 0 for
+        padding)."""
+        if self.groups is not None:
+            if gather_rows or fold_combine or scatter_in_gemm:
+                raise B.MoEError(B.MOE_ERR_UNSUPPORTED,
+                                 "a layer with groups has the default expert path only")
+            B.moe_forward_grouped(self.cfg, self.groups, self.x if x is None else x,
+                                  self.w_router, self.sel_bias, self.logit_offset, token_mask,
+                                  self.weights, self.out if out is None else out, self.topk_idx,
+                                  self.topk_w, self.counts, self.ws, stream=stream)
+            return self.out if out is None else out
+        if token_mask is not None:
+            raise B.MoEError(B.MOE_ERR_UNSUPPORTED, "token_mask needs a layer with groups")
         args = (self.cfg, self.x if x is None else x, self.w_router, self.sel_bias,
                 self.logit_offset, self.weights, self.out if out is None else out,
                 self.topk_idx, self.topk_w, self.counts, self.ws)
@@ -88,10 +105,35 @@ class MoELayer:
                                       device=self.device)}
         for k, v in self.weights.items():
             g["d" + k] = torch.empty_like(v)
-        B.moe_backward(self.cfg, self.x, self.w_router, self.logit_offset, self.weights,
-                       self.topk_idx, self.topk_w, dout, g["dx"], g["dw_router"], g, self.ws,
-                       self.bws, stream)
+        args = (self.x, self.w_router, self.logit_offset, self.weights, self.topk_idx,
+                self.topk_w, dout, g["dx"], g["dw_router"], g, self.ws, self.bws, stream)
+        if self.groups is not None:
+            B.moe_backward_grouped(self.cfg, self.groups, *args)
+        else:
+            B.moe_backward(self.cfg, *args)
         return g
+
+    def orthogonalize(self, grads: Dict[str, torch.Tensor], steps=5, coeffs=B.MUON_COEFFS,
+                      eps=1e-7, scale=1.0, stream=None) -> Dict[str, torch.Tensor]:
+        """Muon's update directions (moe_orthogonalize) of the weight gradients or
+        momenta in ``grads`` (the dw* of backward(), by their names), each in
+        its own dtype; a stacked [E, out, in] tensor is E matrices."""
+        jobs, need = [], 0
+        for k, g in grads.items():
+            if not k.startswith("dw"):
+                continue
+            b, r, c = (1,) * (3 - g.dim()) + tuple(g.shape)
+            dt = B.DTYPE_BF16 if g.dtype == torch.bfloat16 else B.DTYPE_F32
+            cfg = B.make_ortho_config(b, r, c, dt, dt, steps, coeffs, eps, scale)
+            need = max(need, B.moe_orthogonalize_workspace_size(cfg))
+            jobs.append((k, g, cfg))
+        if jobs and (not hasattr(self, "ows") or self.ows.numel() < need):
+            self.ows = torch.empty((max(need, 256),), dtype=torch.uint8, device=self.device)
+        out = {}
+        for k, g, cfg in jobs:
+            out[k] = torch.empty_like(g)
+            B.moe_orthogonalize(cfg, g, out[k], self.ows, stream=stream)
+        return out
 
     def bias_update(self, counts: Optional[torch.Tensor] = None, rate=1e-3, starved_frac=0.1,
                     starved_add=0.5, clamp=10.0, stream=None):

@@ -438,3 +438,93 @@ def moe_backward(inp: dict, top_k: int, gate: int, norm_topk_prob: bool, dout,
     dx += dlogits @ _as64(inp["w_router"])
     out["dx"] = dx
     return out
+
+
+def route_groups(logits, top_k: int, gate: int, norm_topk_prob: bool, sel_bias=None,
+                 n_group: int = 1, topk_group: int = 1, group_score: int = 2,
+                 bias_space: int = 1, scale: float = 1.0, token_mask=None):
+    """Group-limited selection on given logits, token by token.
+
+    The "noaux_tc" router the page-3 model card names without code: experts in
+    n_group groups of consecutive ids; a group scores its largest key
+    (group_score 1) or the sum of its two largest (2; the one where it has
+    one); the topk_group best groups stay, then the top_k best of their
+    experts.  An expert with logit -inf, a score that is not a number or a
+    key of -inf (or NaN) is never picked.  Returns (idx [T, k] with -1 for
+    entries that have no expert, w [T, k] f64, scores [T, E]).
+    """
+    l = _as64(logits)
+    T, E = l.shape
+    per = E // n_group
+    with np.errstate(all="ignore"):
+        s = sigmoid(l) if gate == GATE_SIGMOID else softmax_rows(l)
+        key = (s if bias_space == 1 else l)
+        if sel_bias is not None:
+            key = key + _as64(sel_bias)[None, :]
+        ok = (l > -np.inf) & ~np.isnan(s) & (key > -np.inf)
+    idx = np.full((T, top_k), -1, dtype=np.int64)
+    w = np.zeros((T, top_k))
+    for t in range(T):
+        if token_mask is not None and not token_mask[t]:
+            continue
+        cand = [[e for e in range(g * per, (g + 1) * per) if ok[t, e]] for g in range(n_group)]
+        if topk_group < n_group:
+            score = []
+            for g, es in enumerate(cand):
+                best = sorted((key[t, e] for e in es), reverse=True)[:group_score]
+                if best:
+                    score.append((-sum(best), g))
+            keep = {g for _, g in sorted(score)[:topk_group]}
+        else:
+            keep = set(range(n_group))
+        es = sorted((-key[t, e], e) for g in keep for e in cand[g])[:top_k]
+        for j, (_, e) in enumerate(es):
+            idx[t, j] = e
+            w[t, j] = s[t, e]
+    if norm_topk_prob:
+        w = w / (w.sum(axis=1, keepdims=True) + 1e-9)
+    return idx, w * float(np.float32(scale)), s
+
+
+def route_groups_backward(logits, topk_idx, dw, gate: int, norm_topk_prob: bool,
+                          scale: float = 1.0) -> np.ndarray:
+    """dlogits of <dw, w> of ``route_groups`` by the chain rule; entries of
+    topk_idx outside [0, E) are no pairs, an id listed twice counts twice."""
+    l = _as64(logits)
+    T, E = l.shape
+    c = float(np.float32(scale))
+    out = np.zeros((T, E))
+    for t in range(T):
+        pairs = [(int(e), float(dw[t, j])) for j, e in enumerate(topk_idx[t]) if 0 <= e < E]
+        if not pairs:
+            continue
+        s = sigmoid(l[t]) if gate == GATE_SIGMOID else softmax_rows(l[t])
+        D = sum(s[e] for e, _ in pairs) + 1e-9
+        ds = np.zeros(E)
+        for e, g in pairs:
+            if norm_topk_prob:
+                # g - sum_i g_i s_i / D with D = sum_i s_i + 1e-9, over D
+                num = 1e-9 * g + sum(s[i] * (g - gi) for i, gi in pairs)
+                ds[e] += c * num / D ** 2
+            else:
+                ds[e] += c * g
+        out[t] = ds * s * (1.0 - s) if gate == GATE_SIGMOID else s * (ds - np.dot(ds, s))
+    return out
+
+
+def orthogonalize(g, steps: int = 5, coeffs=(3.4445, -4.7750, 2.0315), eps: float = 1e-7,
+                  scale: float = 1.0) -> np.ndarray:
+    """Newton-Schulz iteration of the Muon optimiser (which the
+    "moe-200m-qwen3-100b" README trains its matrix weights with) on a batch
+    [B, rows, cols]: X = G / (|G|_F + eps), then ``steps`` times
+    X = a X + (b A + c A A) X with A = X X^T; transposed when rows > cols."""
+    a, b, c = (float(np.float32(v)) for v in coeffs)
+    out = []
+    for m in _as64(g):
+        x = m.T if m.shape[0] > m.shape[1] else m
+        x = x / (np.sqrt(np.sum(x * x)) + float(np.float32(eps)))
+        for _ in range(steps):
+            A = x @ x.T
+            x = a * x + (b * A + c * (A @ A)) @ x
+        out.append((x.T if m.shape[0] > m.shape[1] else x) * float(np.float32(scale)))
+    return np.stack(out) if out else _as64(g)
