@@ -67,6 +67,7 @@ struct RouteShape {
   int T, E, k, groups, topk_group, group_score, gate, space, norm;
   float scale;
   long long ld;
+  int per;               // E / groups
 };
 enum class RouteLogits { f32, bf16, f64 };   // f64: forward only
 cudaError_t route_groups(const RouteShape& a, RouteLogits type, const void* logits,

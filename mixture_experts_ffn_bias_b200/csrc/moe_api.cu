@@ -270,7 +270,7 @@ moe_status route_shape(const moe_config* c, const moe_group_opts* o, int64_t ld,
   if (ld < c->n_experts || ld > (int64_t{1} << 31)) return MOE_ERR_INVALID;
   *s = moe::RouteShape{c->T,    c->n_experts,  c->top_k,          o->n_group,
                        o->topk_group, o->group_score, c->gate, o->bias_space,
-                       c->norm_topk_prob, o->scale, ld};
+                       c->norm_topk_prob, o->scale, ld, c->n_experts / o->n_group};
   return MOE_OK;
 }
 

@@ -11,8 +11,10 @@
 //   the topk_group best groups stay, then the top_k best of their experts;
 //   w = scale s / (sum of the chosen s + 1e-9), or scale s.
 // The selection is the one fp64 keys give, ties to the lower id.  Keys are
-// compared in fp32 first; a token where two compared values are closer than
-// their fp32 error is decided again in fp64 (a few in a thousand).
+// compared in fp32 first.  Picks whose keys are closer than their fp32 error
+// are put in order by fp64 keys of theirs alone (a few tokens in a thousand);
+// a token whose groups are that close, or with values fp32 cannot rank, is
+// decided again as a whole in fp64.
 //
 // Bound by memory for many tokens (the logits are read once), by the
 // selection's instructions close behind: 4 tokens per warp, 8 lanes each, so
@@ -45,6 +47,63 @@ __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) {
   return __bfloat162float(v);
 }
 
+// Shared-memory position of expert e: 4 floats of padding per 32, so that
+// the 8 lanes of a token, a group or E/8 experts apart, read 16-byte pieces
+// from different banks.  And the expert at a position (below 36 * 8): p / 36
+// as a multiplication.
+__device__ __forceinline__ int at(int e) { return e + ((e >> 5) << 2); }
+__device__ __forceinline__ int expert_at(int p) { return p - 4 * ((p * 1821) >> 16); }
+
+// A key above -inf as an integer in the keys' order, never 0.
+__device__ __forceinline__ unsigned long long ordered(double v) {
+  const long long b = __double_as_longlong(v + 0.0);   // -0 as 0
+  return static_cast<unsigned long long>(b < 0 ? ~b : b | (1ll << 63));
+}
+
+// The fp64 score of a logit of a row: (m, sum) of the softmax, by one warp.
+template <typename L>
+__device__ __forceinline__ void softmax_f64(const RouteShape& a, const L* __restrict__ row,
+                                            int lane, double& m, double& sum) {
+  m = -INFINITY;
+  for (int e = lane; e < a.E; e += 32) m = fmax(m, to_f64(row[e]));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(kFull, m, o));
+  if (m == -INFINITY) m = 0.0;
+  sum = 0.0;
+  for (int e = lane; e < a.E; e += 32) sum += exp(to_f64(row[e]) - m);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+}
+
+// The `count` <= 32 best experts of one token by fp32 keys (picks: position,
+// key), put into the order of their fp64 keys by the whole warp: each lane
+// counts the better ones.
+template <typename L>
+__device__ __noinline__ void order_picks_f64(const RouteShape& a, const L* __restrict__ row,
+                                             const float* __restrict__ bias, int lane, int count,
+                                             int2* picks) {
+  double m = 0.0, sum = 1.0;
+  if (a.gate == 0 && a.space == 1) softmax_f64(a, row, lane, m, sum);
+  int2 p = make_int2(1 << 30, 0);
+  double key = -INFINITY;
+  if (lane < count) {
+    p = picks[lane];
+    const int e = expert_at(p.x);
+    key = to_f64(row[e]);
+    if (a.space == 1) key = a.gate == 0 ? exp(key - m) / sum : 1.0 / (1.0 + exp(-key));
+    if (bias != nullptr) key += static_cast<double>(bias[e]);
+  }
+  int rank = 0;
+  for (int j = 0; j < count; ++j) {
+    const double o = __shfl_sync(kFull, key, j);
+    const int oe = __shfl_sync(kFull, p.x, j);
+    rank += (o > key || (o == key && oe < p.x)) ? 1 : 0;
+  }
+  __syncwarp();
+  if (lane < count) picks[rank] = p;
+  __syncwarp();
+}
+
 // One token by one warp, in fp64.  skey: E doubles of shared memory.
 template <typename L>
 __device__ __noinline__ void route_token_f64(const RouteShape& a, const L* __restrict__ row,
@@ -53,17 +112,7 @@ __device__ __noinline__ void route_token_f64(const RouteShape& a, const L* __res
                                              float* __restrict__ topk_w) {
   const double ninf = -INFINITY;
   double m = 0.0, sum = 1.0;
-  if (a.gate == 0) {
-    m = ninf;
-    for (int e = lane; e < a.E; e += 32) m = fmax(m, to_f64(row[e]));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(kFull, m, o));
-    if (m == ninf) m = 0.0;
-    sum = 0.0;
-    for (int e = lane; e < a.E; e += 32) sum += exp(to_f64(row[e]) - m);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-  }
+  if (a.gate == 0) softmax_f64(a, row, lane, m, sum);
   auto score = [&](double l) {
     return a.gate == 0 ? exp(l - m) / sum : 1.0 / (1.0 + exp(-l));
   };
@@ -76,7 +125,7 @@ __device__ __noinline__ void route_token_f64(const RouteShape& a, const L* __res
     skey[e] = ok ? key : ninf;
   }
   __syncwarp();
-  const int per = a.E / a.groups;
+  const int per = a.per;
   unsigned use = kFull;
   if (a.topk_group < a.groups) {
     double sc = ninf;
@@ -95,23 +144,32 @@ __device__ __noinline__ void route_token_f64(const RouteShape& a, const L* __res
     }
     use = __ballot_sync(kFull, lane < a.groups && rank < a.topk_group);
   }
-  int mine = -1;
-  for (int j = 0; j < a.k; ++j) {
+  // each lane's best expert as an ordered integer; only the round's winner
+  // looks again
+  int mine = -1, be = kMaxE;
+  unsigned long long ob = 0;
+  auto look = [&]() {
     double best = ninf;
-    int be = kMaxE;
+    be = kMaxE;
     for (int e = lane; e < a.E; e += 32) {
       const double v = skey[e];
       if (v > best && ((use >> (a.topk_group < a.groups ? e / per : 0)) & 1u)) { best = v; be = e; }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const double v = __shfl_xor_sync(kFull, best, o);
-      const int e = __shfl_xor_sync(kFull, be, o);
-      if (v > best || (v == best && e < be)) { best = v; be = e; }
+    ob = be < kMaxE ? ordered(best) : 0ull;
+  };
+  look();
+  for (int j = 0; j < a.k; ++j) {
+    const unsigned h = static_cast<unsigned>(ob >> 32);
+    const unsigned mh = __reduce_max_sync(kFull, h);
+    if (mh == 0u) break;                 // nothing eligible is left
+    const unsigned l = h == mh ? static_cast<unsigned>(ob) : 0u;
+    const unsigned ml = __reduce_max_sync(kFull, l);
+    const int e = __reduce_min_sync(kFull, h == mh && l == ml ? be : kMaxE);
+    if (lane == j) mine = e;
+    if (be == e) {
+      skey[e] = ninf;
+      look();
     }
-    if (be >= kMaxE) break;              // nothing eligible is left
-    if (lane == j) mine = be;
-    if ((be & 31) == lane) skey[be] = ninf;
   }
   double s = mine >= 0 ? score(to_f64(row[mine])) : 0.0;
   double tot = s;
@@ -149,29 +207,72 @@ route_f64_kernel(const RouteShape a, const L* __restrict__ logits, const float* 
                      topk_idx, topk_w);
 }
 
-__device__ __forceinline__ float fast_sigmoid(float l) {
-  return __fdividef(1.0f, 1.0f + __expf(-l));
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// e^x within (2 + 1.16 |x|) 2^-23 of itself, below 2^-126 as 0.
+__device__ __forceinline__ float fast_exp(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+  return r;
 }
 
-// Shared-memory position of expert e: 4 floats of padding per 32, so that
-// the 8 lanes of a token, E/8 experts apart, read 16-byte pieces from
-// different banks.
-__device__ __forceinline__ int at(int e) { return e + ((e >> 5) << 2); }
+// Within 2.5e-7 of the sigmoid: s (1 - s) turns the exponential's error into
+// 7e-8; sum and reciprocal add 1.8e-7 s.
+__device__ __forceinline__ float fast_sigmoid(float l) {
+  return rcp_approx(1.0f + fast_exp(-l));
+}
 
-// 4 tokens per warp, 8 lanes per token.  NB = ceil(E / 32): lane `sub` of a
-// token owns the experts [4 NB sub, 4 NB (sub + 1)).
-template <typename L, int NB>
-__global__ void __launch_bounds__(256)
+// Four consecutive logits of a row; VEC: one aligned load.
+template <typename L, bool VEC>
+__device__ __forceinline__ float4 load4(const L* __restrict__ row, int e, int E) {
+  const float ninf = -INFINITY;
+  if constexpr (VEC) {
+    if (e >= E) return make_float4(ninf, ninf, ninf, ninf);
+    if constexpr (sizeof(L) == 4) {
+      return __ldg(reinterpret_cast<const float4*>(row + e));
+    } else {
+      const uint2 q = __ldg(reinterpret_cast<const uint2*>(row + e));
+      const float2 lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&q.x));
+      const float2 hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&q.y));
+      return make_float4(lo.x, lo.y, hi.x, hi.y);
+    }
+  } else {
+    return make_float4(e < E ? to_f32<L>(row[e]) : ninf, e + 1 < E ? to_f32<L>(row[e + 1]) : ninf,
+                       e + 2 < E ? to_f32<L>(row[e + 2]) : ninf,
+                       e + 3 < E ? to_f32<L>(row[e + 3]) : ninf);
+  }
+}
+
+constexpr int kRouteWarps = 4;
+constexpr int kPickRow = kMaxK + 2;
+
+// 4 tokens per warp, 8 lanes per token (`sub` of `tok`).
+//   1  the warp forms one token's keys after another (lanes own 4 experts
+//      each) and leaves them in shared memory
+//   2  lane `sub` scans the groups sub, sub + 8, ..: two largest, score; the
+//      groups are ranked by counting the better ones
+//   3  the chosen groups' experts are dealt out to the 8 lanes in ascending
+//      order; the maximum of each 4 experts sits in a register, and a round
+//      of the top-k is the maximum over a lane's registers, three shuffles,
+//      and the winner's new block maximum
+//   4  weights
+// NB: blocks of 4 experts of a lane in step 3, rounded up to a power of two.
+template <typename L, int NB, bool VEC>
+__global__ void __launch_bounds__(32 * kRouteWarps, 8)
 route_kernel(const RouteShape a, const L* __restrict__ logits, const float* __restrict__ bias,
              const uint8_t* __restrict__ mask, int32_t* __restrict__ topk_idx,
              float* __restrict__ topk_w) {
   pdl_trigger();
   pdl_wait();
-  constexpr int ROW = 36 * NB;               // floats of a token's keys in shared memory
-  extern __shared__ float smem[];
+  extern __shared__ __align__(16) float smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane & 7, tok = lane >> 3;
-  float* keys = smem + warp * 4 * ROW;
+  const int ROW = 36 * ((a.E + 31) / 32);    // floats of a token's keys
+  float* keys = smem + warp * (4 * ROW + 8 * kPickRow);
+  int2* picks = reinterpret_cast<int2*>(keys + 4 * ROW) + tok * kPickRow;
   const int t0 = (blockIdx.x * (blockDim.x >> 5) + warp) * 4;
   if (t0 >= a.T) return;
   const float ninf = -INFINITY;
@@ -179,126 +280,156 @@ route_kernel(const RouteShape a, const L* __restrict__ logits, const float* __re
   // theirs (no bias), else the biased keys
   const bool biased = bias != nullptr;
   const bool by_score = a.space == 1 && biased;   // keys = s + bias
-  unsigned slow = 0;                              // bit r: token r of the four
+  unsigned slow = 0;                              // byte r, not 0: token r by fp64 as a whole
   unsigned live = 0;
   float row_m = 0.f, row_inv = 1.f;               // softmax of this lane's token
+  const int padded = (a.E + 31) & ~31;
+  // ---------------------------------------------------------------- 1 keys
+  float b[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int e = 4 * lane + 128 * (i >> 2) + (i & 3);
+    b[i] = 0.f;
+    if (biased && e < a.E) {
+      b[i] = bias[e];
+      if (!(b[i] == b[i])) b[i] = ninf;           // a NaN switches the expert off
+    }
+  }
+  {
+    const bool on = lane < 4 && t0 + lane < a.T && (mask == nullptr || mask[t0 + lane] != 0);
+    live = __ballot_sync(kFull, on);
+  }
 #pragma unroll 1
-  for (int r = 0; r < 4; ++r) {
-    const int t = t0 + r;
-    const bool on = t < a.T && (mask == nullptr || mask[t] != 0);   // warp-uniform
-    if (!on) continue;
-    live |= 1u << r;
-    const L* row = logits + static_cast<size_t>(t) * a.ld;
-    float l[NB];
+  for (int r2 = 0; r2 < 4; r2 += 2) {
+    float4 lv[2][2];
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      const int e = lane + 32 * i;
-      l[i] = e < a.E ? to_f32<L>(row[e]) : ninf;
-    }
-    bool odd = false;                             // a value only fp64 decides
-    float m = 0.f, inv = 1.f;
-    if (a.gate == 0) {
-      m = ninf;
+    for (int q = 0; q < 2; ++q) {
+      const L* row = logits + static_cast<size_t>(t0 + r2 + q) * a.ld;
+      const bool on = (live >> (r2 + q)) & 1u;
 #pragma unroll
-      for (int i = 0; i < NB; ++i) m = fmaxf(m, l[i]);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-      float s = 0.f;
-#pragma unroll
-      for (int i = 0; i < NB; ++i) s += __expf(l[i] - m);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
-      odd = !(s >= 0.5f && s <= 1024.f);          // NaN, +inf, or no finite logit
-      inv = 1.0f / s;
-    } else if (!by_score) {
-      // NaN or +inf; beyond 16 distinct logits may have equal fp64 sigmoids
-      const float most = a.space == 1 ? 16.f : 1e30f;
-#pragma unroll
-      for (int i = 0; i < NB; ++i) odd = odd || !(l[i] <= most);
+      for (int i = 0; i < 2; ++i) {
+        const int e = 4 * lane + 128 * i;
+        lv[q][i] = make_float4(ninf, ninf, ninf, ninf);
+        if (on && e < a.E) lv[q][i] = load4<L, VEC>(row, e, a.E);
+      }
     }
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      const int e = lane + 32 * i;
-      float key = l[i];
-      if (by_score) key = a.gate == 0 ? __expf(l[i] - m) * inv : fast_sigmoid(l[i]);
-      if (biased && e < a.E) key += bias[e];
-      if (!(key > ninf) || !(l[i] > ninf)) key = ninf;
-      keys[r * ROW + at(e)] = key;
+    for (int q = 0; q < 2; ++q) {
+      const int r = r2 + q;
+      if (!((live >> r) & 1u)) continue;          // warp-uniform
+      float* l = reinterpret_cast<float*>(lv[q]);
+      bool odd = false;                           // values only fp64 decides
+      if (a.gate == 0) {
+        float m = ninf, s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, l[i]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          x[i] = fast_exp(l[i] - m);
+          s += x[i];
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+        odd = !(s >= 0.5f && s <= 1024.f);        // NaN, +inf, or no finite logit
+        const float inv = rcp_approx(s);
+        if (tok == r) { row_m = m; row_inv = inv; }
+        if (by_score) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) l[i] = l[i] > ninf ? fmaf(x[i], inv, b[i]) : ninf;
+        }
+      } else if (by_score) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) l[i] = l[i] > ninf ? fast_sigmoid(l[i]) + b[i] : ninf;
+      } else {
+        // NaN or +inf; beyond 16 distinct logits may have equal fp64 sigmoids
+        const float most = a.space == 1 ? 16.f : 1e30f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) odd = odd || !(l[i] <= most);
+      }
+      if (biased && !by_score) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) l[i] = l[i] > ninf ? l[i] + b[i] : ninf;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int e = 4 * lane + 128 * i;
+        if (e < padded) *reinterpret_cast<float4*>(keys + r * ROW + at(e)) = lv[q][i];
+      }
+      if (__any_sync(kFull, odd)) slow |= 0xffu << (8 * r);
     }
-    if (__any_sync(kFull, odd)) slow |= 1u << r;
-    if (tok == r) { row_m = m; row_inv = inv; }
   }
   __syncwarp();
   float* mykeys = keys + tok * ROW;
-  const int per = a.E / a.groups;
+  const int per = a.per;
   const bool limited = a.topk_group < a.groups;
-  unsigned use = kFull;                           // groups this lane's token may use
+  const bool whole = (per & 3) == 0;              // groups are whole blocks of 4
+  const float inv_per = rcp_approx(static_cast<float>(per));   // of small integers only
+  // -------------------------------------------------------------- 2 groups
   if (limited) {
     // a score's fp32 error: none for the largest of unbiased logits, relative
     // for sums of exponentials, else that of keys formed from fp32 scores
-    float sc[4], err[4];
-    float lo = INFINITY, hi = ninf;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int g = sub + 8 * i;
-      sc[i] = ninf;
-      err[i] = 0.f;
-      if (8 * i >= a.groups) continue;            // warp-uniform
-      if (g < a.groups) {
-        float m1 = ninf, m2 = ninf;
-        if ((per & 3) == 0) {
-          for (int e = g * per; e < (g + 1) * per; e += 4) {
-            const float4 q = *reinterpret_cast<const float4*>(mykeys + at(e));
-            m2 = fmaxf(m2, fminf(m1, q.x)); m1 = fmaxf(m1, q.x);
-            m2 = fmaxf(m2, fminf(m1, q.y)); m1 = fmaxf(m1, q.y);
-            m2 = fmaxf(m2, fminf(m1, q.z)); m1 = fmaxf(m1, q.z);
-            m2 = fmaxf(m2, fminf(m1, q.w)); m1 = fmaxf(m1, q.w);
-          }
-        } else {
-          for (int e = g * per; e < (g + 1) * per; ++e) {
-            const float v = mykeys[at(e)];
-            m2 = fmaxf(m2, fminf(m1, v));
-            m1 = fmaxf(m1, v);
-          }
+#pragma unroll 1
+    for (int g = sub; g < a.groups; g += 8) {
+      float m1 = ninf, m2 = ninf;
+      if (whole) {
+#pragma unroll 2
+        for (int e = g * per; e < (g + 1) * per; e += 4) {
+          const float4 q = *reinterpret_cast<const float4*>(mykeys + at(e));
+          const float h1 = fmaxf(q.x, q.y), l1 = fminf(q.x, q.y);
+          const float h2 = fmaxf(q.z, q.w), l2 = fminf(q.z, q.w);
+          const float h = fmaxf(h1, h2);
+          const float second = fmaxf(fmaxf(fminf(h1, h2), l1), l2);
+          m2 = fmaxf(fmaxf(fminf(m1, h), second), m2);
+          m1 = fmaxf(m1, h);
         }
-        sc[i] = m1;
-        const bool two = a.group_score == 2 && m2 > ninf;
-        if (a.group_score == 2 && a.space == 1 && !biased && m1 > ninf) {
-          // sums of scores; the softmax's divisor is common to all groups
-          if (a.gate == 0) {
-            sc[i] = expf(m1 - row_m) + expf(m2 - row_m);
-            err[i] = 1e-5f * sc[i];
-          } else {
-            sc[i] = 1.0f / (1.0f + expf(-m1)) + (two ? 1.0f / (1.0f + expf(-m2)) : 0.f);
-            err[i] = 2e-6f;
-          }
-        } else if (biased || two) {
-          if (two) sc[i] = m1 + m2;
-          err[i] = 4e-6f * (1.f + fabsf(m1) + (two ? fabsf(m2) : 0.f));
+      } else {
+        for (int e = g * per; e < (g + 1) * per; ++e) {
+          const float v = mykeys[at(e)];
+          m2 = fmaxf(m2, fminf(m1, v));
+          m1 = fmaxf(m1, v);
         }
       }
-    }
-    use = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (8 * i >= a.groups) continue;
-      const int g = sub + 8 * i;
-      int rank = 0;
-#pragma unroll
-      for (int ih = 0; ih < 4; ++ih) {
-        if (8 * ih >= a.groups) continue;
-#pragma unroll
-        for (int hl = 0; hl < 8; ++hl) {
-          const int h = hl + 8 * ih;
-          const float o = __shfl_sync(kFull, sc[ih], (tok << 3) | hl);
-          if (h < a.groups) rank += (o > sc[i] || (o == sc[i] && h < g)) ? 1 : 0;
+      float sc = m1, err = 0.f;
+      const bool two = a.group_score == 2 && m2 > ninf;
+      if (a.group_score == 2 && a.space == 1 && !biased) {
+        // sums of scores; the softmax's divisor is common to all groups
+        if (m1 > ninf) {
+          if (a.gate == 0) {
+            sc = expf(m1 - row_m) + expf(m2 - row_m);
+            err = 1e-5f * sc;
+          } else {
+            sc = fast_sigmoid(m1) + (two ? fast_sigmoid(m2) : 0.f);
+            err = 1.2e-6f;
+          }
         }
+      } else if (biased || two) {
+        if (two) sc = m1 + m2;
+        err = 1.2e-6f + 2e-7f * (fabsf(m1) + (two ? fabsf(m2) : 0.f));
+      }
+      picks[g] = make_int2(__float_as_int(err), __float_as_int(sc));
+    }
+    __syncwarp();
+    unsigned use = 0;
+    float lo = INFINITY, hi = ninf;
+#pragma unroll 1
+    for (int i = 0; 8 * i < a.groups; ++i) {
+      const int g = sub + 8 * i;
+      const int2 own = picks[g < a.groups ? g : 0];
+      const float sc = __int_as_float(own.y), err = __int_as_float(own.x);
+      int rank = 0;
+#pragma unroll 4
+      for (int h = 0; h < a.groups; ++h) {
+        const float o = __int_as_float(picks[h].y);
+        rank += (o > sc || (o == sc && h < g)) ? 1 : 0;
       }
       const bool in = g < a.groups && rank < a.topk_group;
       const unsigned bits = __ballot_sync(kFull, in);
       use |= ((bits >> (tok << 3)) & 0xffu) << (8 * i);
-      if (g < a.groups && sc[i] > ninf) {
-        if (in) lo = fminf(lo, sc[i] - err[i]); else hi = fmaxf(hi, sc[i] + err[i]);
+      if (g < a.groups && sc > ninf) {
+        if (in) lo = fminf(lo, sc - err); else hi = fmaxf(hi, sc + err);
       }
     }
 #pragma unroll
@@ -314,45 +445,51 @@ route_kernel(const RouteShape a, const L* __restrict__ logits, const float* __re
       near = a.space == 1 && hi > ninf &&
              ((lo > hi && lo - hi < 1e-7f) || lo < (a.gate == 0 ? row_m - 700.f : -700.f));
     }
-    const unsigned nb = __ballot_sync(kFull, near);
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if ((nb >> (8 * r)) & 0xffu) slow |= 1u << r;
+    slow |= __ballot_sync(kFull, near);           // (the shuffles were warp barriers)
+    if (whole) {
+      // the chosen groups in ascending order
+#pragma unroll 1
+      for (int g = sub; g < a.groups; g += 8)
+        if ((use >> g) & 1u) picks[__popc(use & ((1u << g) - 1u))].x = g * per;
+    } else {
+      for (int e = sub; e < a.E; e += 8) {
+        const int g = static_cast<int>((e + 0.5f) * inv_per);
+        if (!((use >> g) & 1u)) mykeys[at(e)] = ninf;
+      }
+    }
+    __syncwarp();
   }
 
-  // top-k: the maximum of each 4 experts in registers
-  const bool alive = (live >> tok) & 1u;
-  const float inv_per = 1.0f / static_cast<float>(per);
+  // --------------------------------------------------------------- 3 top-k
+  const bool alive = ((live >> tok) & 1u) && ((slow >> (8 * tok)) & 0xffu) == 0u;
+  const int total = limited && whole ? a.topk_group * per : a.E;   // experts to choose from
+  const int nbr = (total + 31) >> 5;               // blocks of 4 of a lane
+  // where the lane's block i lies in the token's keys; blocks that are not
+  // there point at the first and have no maximum
+  int base[NB];
   float bm[NB];
 #pragma unroll
   for (int i = 0; i < NB; ++i) {
-    const int e = 4 * (NB * sub + i);
-    float4 q = *reinterpret_cast<const float4*>(mykeys + at(e));
-    if (limited) {
-      float* f = reinterpret_cast<float*>(&q);
-      if ((per & 3) == 0) {
-        const int g = static_cast<int>((e + 0.5f) * inv_per);
-        if (!((use >> (g & 31)) & 1u)) q = make_float4(ninf, ninf, ninf, ninf);
-      } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int g = static_cast<int>((e + c + 0.5f) * inv_per);
-          if (!((use >> (g & 31)) & 1u)) f[c] = ninf;
-        }
-        *reinterpret_cast<float4*>(mykeys + at(e)) = q;
+    const int p = 4 * (nbr * sub + i);
+    base[i] = 0;
+    bm[i] = ninf;
+    if (alive && i < nbr && p < total) {
+      int e = p;
+      if (limited && whole) {
+        const int gi = static_cast<int>((p + 0.5f) * inv_per);
+        e = picks[gi].x + p - gi * per;
       }
+      base[i] = at(e);
+      const float4 q = *reinterpret_cast<const float4*>(mykeys + base[i]);
+      bm[i] = fmaxf(fmaxf(q.x, q.y), fmaxf(q.z, q.w));
     }
-    bm[i] = alive ? fmaxf(fmaxf(q.x, q.y), fmaxf(q.z, q.w)) : ninf;
   }
   __syncwarp();
-  int pick[kMaxK / 8];
-#pragma unroll
-  for (int i = 0; i < kMaxK / 8; ++i) pick[i] = -1;
-  float prev = INFINITY;
-  int prev_e = 0;
-  bool near = false;
-  const bool check = biased || a.space == 1;
-  for (int j = 0; j <= a.k; ++j) {   // one more than k: is the last one's lead clear
+  const unsigned lower = (0xffu << (tok << 3)) & ((1u << lane) - 1u);   // this token's lower lanes
+  int count = 0;
+  // pick j: (place in the token's keys, key).  Written without branches: the
+  // four tokens' winners sit at different places.
+  auto round = [&](int j) {
     float lm = bm[0];
 #pragma unroll
     for (int i = 1; i < NB; ++i) lm = fmaxf(lm, bm[i]);
@@ -360,200 +497,315 @@ route_kernel(const RouteShape a, const L* __restrict__ logits, const float* __re
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(kFull, best, o));
     const bool any = best > ninf;
-    const unsigned who = (__ballot_sync(kFull, lm == best) >> (tok << 3)) & 0xffu;
-    const int wsub = __ffs(who) - 1;         // lanes own ascending experts
-    int e = 0;
-    if (any && sub == wsub) {
-      int blk = 0;
+    // lanes own ascending experts, so the lowest lane has the lowest id
+    const unsigned who = __ballot_sync(kFull, lm == best);
+    const bool win = any && lm == best && (who & lower) == 0u;
+    count += any ? 1 : 0;
+    int ix = base[NB - 1];
 #pragma unroll
-      for (int i = NB - 1; i >= 0; --i)
-        if (bm[i] == best) blk = i;
-      const int e0 = 4 * (NB * sub + blk);
-      float* kp = mykeys + at(e0);
-      float4 q = *reinterpret_cast<const float4*>(kp);
-      int c = 3;
-      if (q.z == best) c = 2;
-      if (q.y == best) c = 1;
-      if (q.x == best) c = 0;
-      e = e0 + c;
-      kp[c] = ninf;
-      if (c == 0) q.x = ninf;
-      if (c == 1) q.y = ninf;
-      if (c == 2) q.z = ninf;
-      if (c == 3) q.w = ninf;
-      const float nm = fmaxf(fmaxf(q.x, q.y), fmaxf(q.z, q.w));
-#pragma unroll
-      for (int i = 0; i < NB; ++i)
-        if (i == blk) bm[i] = nm;
+    for (int i = NB - 2; i >= 0; --i) ix = bm[i] == best ? base[i] : ix;
+    const float4 q = *reinterpret_cast<const float4*>(mykeys + ix);
+    int c = q.z == best ? 2 : 3;
+    c = q.y == best ? 1 : c;
+    c = q.x == best ? 0 : c;
+    const float nm = fmaxf(fmaxf(c == 0 ? ninf : q.x, c == 1 ? ninf : q.y),
+                           fmaxf(c == 2 ? ninf : q.z, c == 3 ? ninf : q.w));
+    if (win) {
+      picks[j] = make_int2(ix + c, __float_as_int(best));
+      mykeys[ix + c] = ninf;
     }
-    e = __shfl_sync(kFull, e, (tok << 3) | (any ? wsub : 0));
-    if (any && check) {
-      const float gap = prev - best;
-      if (biased) {
-        // keys formed in fp32; equal inputs are an exact tie
-        if (!(gap > 2e-6f * (1.f + fabsf(best)))) {
-          const L* row = logits + static_cast<size_t>(t0 + tok) * a.ld;
-          near = near || !(to_f32<L>(row[e]) == to_f32<L>(row[prev_e]) &&
-                           bias[e] == bias[prev_e]);
-        }
-      } else if ((gap > 0.f && gap < 1e-7f) || prev < (a.gate == 0 ? row_m - 700.f : -700.f)) {
+#pragma unroll
+    for (int i = 0; i < NB; ++i) bm[i] = win && base[i] == ix ? nm : bm[i];
+  };
+  for (int j = 0; j <= a.k; ++j) round(j);   // one more than k: is the last one's lead clear
+  __syncwarp();
+  // the logit of the lane's first pick, asked for before it is needed
+  const int t = t0 + tok;
+  float first = 0.f;
+  bool moved = false;
+  if (biased && sub < count)
+    first = to_f32<L>(logits[static_cast<size_t>(t) * a.ld + expert_at(picks[sub].x)]);
+  // ---------------------------------------------- are the leads clear in fp32
+  if (biased || a.space == 1) {
+    // whether picks j and j + 1 are
+    auto close = [&](int j) {
+      const int2 p = picks[j], n = picks[j + 1];
+      const float best = __int_as_float(p.y), gap = best - __int_as_float(n.y);
+      if (!biased)
+        return (gap > 0.f && gap < 1e-7f) || best < (a.gate == 0 ? row_m - 700.f : -700.f);
+      if (gap > 1.5e-6f + 2.5e-7f * fabsf(best)) return false;
+      // keys formed in fp32; equal inputs are an exact tie
+      const L* row = logits + static_cast<size_t>(t0 + tok) * a.ld;
+      const int e = expert_at(p.x), f = expert_at(n.x);
+      return !(to_f32<L>(row[e]) == to_f32<L>(row[f]) && bias[e] == bias[f]);
+    };
+    bool near = false, edge = false;
+    for (int j = sub; j + 1 < count; j += 8)
+      if (close(j)) {
         near = true;
+        edge = edge || j + 1 == a.k;
+      }
+    unsigned fix = __ballot_sync(kFull, near);
+    if (fix != 0u) {   // warp-uniform
+      moved = true;
+      unsigned again = 0;
+      if (__any_sync(kFull, edge)) {
+        // the best one left out is as close: is the next one clear
+        const int before = count;
+        round(a.k + 1);
+        __syncwarp();
+        again = __ballot_sync(kFull, edge && count > before && close(a.k));
+        // (a tie further down: the whole token in fp64)
+      }
+      const unsigned many = __ballot_sync(kFull, count > 32);
+#pragma unroll 1
+      for (int r = 0; r < 4; ++r) {
+        if (!((fix >> (8 * r)) & 0xffu)) continue;
+        if (((again | many) >> (8 * r)) & 0xffu)
+          slow |= 0xffu << (8 * r);
+        else
+          order_picks_f64<L>(a, logits + static_cast<size_t>(t0 + r) * a.ld, bias, lane,
+                             __shfl_sync(kFull, count, 8 * r), picks + (r - tok) * kPickRow);
       }
     }
-    prev = best;
-    prev_e = e;
-#pragma unroll
-    for (int i = 0; i < kMaxK / 8; ++i)
-      if (any && j < a.k && j == sub + 8 * i) pick[i] = e;
-    if (!__any_sync(kFull, any)) break;
   }
-  const unsigned nb = __ballot_sync(kFull, near);
-#pragma unroll
-  for (int r = 0; r < 4; ++r)
-    if ((nb >> (8 * r)) & 0xffu) slow |= 1u << r;
-  slow &= live;
+  // padding tokens are not decided at all
+  slow &= 0xffu * ((live & 1u) | (live & 2u) << 7 | (live & 4u) << 14 | (live & 8u) << 21);
 
-  // weights: lane `sub` has the picks sub, sub + 8, ..
-  const int t = t0 + tok;
-  float s[kMaxK / 8];
+  // ------------------------------------------------------------- 4 weights
+  const int n = count < a.k ? count : a.k;
   float tot = 0.f;
-#pragma unroll
-  for (int i = 0; i < kMaxK / 8; ++i) {
-    s[i] = 0.f;
-    if (pick[i] >= 0) {
-      const float l = to_f32<L>(logits[static_cast<size_t>(t) * a.ld + pick[i]]);
-      s[i] = a.gate == 0 ? expf(l - row_m) * row_inv : 1.0f / (1.0f + expf(-l));
-    }
-    tot += s[i];
+#pragma unroll 1
+  for (int j = sub; j < n; j += 8) {
+    const int2 p = picks[j];
+    const int e = expert_at(p.x);
+    // without a bias the key is the logit
+    float l = __int_as_float(p.y);
+    if (biased)
+      l = j == sub && !moved ? first : to_f32<L>(logits[static_cast<size_t>(t) * a.ld + e]);
+    const float s =
+        a.gate == 0 ? expf(l - row_m) * row_inv : rcp_approx(1.0f + expf(-l));
+    picks[j] = make_int2(e, __float_as_int(s));
+    tot += s;
   }
 #pragma unroll
   for (int o = 4; o > 0; o >>= 1) tot += __shfl_xor_sync(kFull, tot, o);
-  if (t < a.T && !((slow >> tok) & 1u)) {
-    const float f = a.norm ? a.scale / (tot + 1e-9f) : a.scale;
-#pragma unroll
-    for (int i = 0; i < kMaxK / 8; ++i) {
-      const int j = sub + 8 * i;
-      if (j < a.k) {
-        topk_idx[static_cast<size_t>(t) * a.k + j] = pick[i];
-        topk_w[static_cast<size_t>(t) * a.k + j] = pick[i] >= 0 ? s[i] * f : 0.f;
-      }
+  if (t < a.T && ((slow >> (8 * tok)) & 0xffu) == 0u) {
+    const float f = a.norm ? __fdividef(a.scale, tot + 1e-9f) : a.scale;
+    int32_t* idx_row = topk_idx + static_cast<size_t>(t) * a.k;
+    float* w_row = topk_w + static_cast<size_t>(t) * a.k;
+#pragma unroll 1
+    for (int j = sub; j < a.k; j += 8) {
+      const int2 p = picks[j];
+      idx_row[j] = j < n ? p.x : -1;
+      w_row[j] = j < n ? __int_as_float(p.y) * f : 0.f;
     }
   }
   __syncwarp();
-  while (slow != 0) {   // warp-uniform
-    const int r = __ffs(slow) - 1;
-    slow &= slow - 1;
-    route_token_f64<L>(a, logits + static_cast<size_t>(t0 + r) * a.ld, bias, t0 + r, lane,
-                       reinterpret_cast<double*>(keys), topk_idx, topk_w);
-  }
+#pragma unroll 1
+  for (int r = 0; r < 4; ++r)   // warp-uniform
+    if ((slow >> (8 * r)) & 0xffu)
+      route_token_f64<L>(a, logits + static_cast<size_t>(t0 + r) * a.ld, bias, t0 + r, lane,
+                         reinterpret_cast<double*>(keys), topk_idx, topk_w);
 }
 
-// dlogits of one token per warp.  For the chosen experts with scores s_j and
+// dlogits, 4 tokens per warp.  For the chosen experts with scores s_j and
 // incoming dw_j:  ds_j = c (dw_j - sum_i dw_i s_i / D) / D with
 // D = sum_i s_i + 1e-9, or c dw_j;  sigmoid: dl = ds s (1 - s);  softmax:
 // dl_e = p_e (ds_e - sum_j ds_j p_j).  The sums over the chosen experts are in
 // fp64: with one expert a token the difference is 1e-9 of its terms.
-template <typename L, int NB>
-__global__ void __launch_bounds__(256)
+//   1  (softmax) the warp reads one token's row after another and leaves the
+//      exponentials in shared memory
+//   2  lane `sub` of a token takes the pairs sub, sub + 8, ..
+//   3  the rows without the chosen experts' own part (sigmoid: zeros), then
+//      the chosen elements over them
+// Memory bound: a row is read (softmax) and written once.
+template <typename L, bool VEC>
+__global__ void __launch_bounds__(32 * kRouteWarps)
 route_bwd_kernel(const RouteShape a, const L* __restrict__ logits,
                  const int32_t* __restrict__ topk_idx, const float* __restrict__ dw,
                  L* __restrict__ dlogits, long long dld) {
   pdl_trigger();
   pdl_wait();
-  __shared__ float rowbuf[8][32 * NB];
+  extern __shared__ __align__(16) float smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t = blockIdx.x * (blockDim.x >> 5) + warp;
-  if (t >= a.T) return;
-  float* buf = rowbuf[warp];
-  const L* row = logits + static_cast<size_t>(t) * a.ld;
-  int e = -1;
-  float d = 0.f;
-  if (lane < a.k) {
-    e = topk_idx[static_cast<size_t>(t) * a.k + lane];
-    if (e < 0 || e >= a.E) e = -1;
-    if (e >= 0) d = dw[static_cast<size_t>(t) * a.k + lane];
-  }
-  float l[NB], p[NB];
-  float m = 0.f, inv = 1.f;
-  if (a.gate == 0) {
-    m = -INFINITY;
+  const int sub = lane & 7, tok = lane >> 3;
+  const int ROW = (a.E + 3) & ~3;
+  float* rows = smem + warp * (4 * ROW + 32);
+  unsigned* seen = reinterpret_cast<unsigned*>(rows + 4 * ROW);   // 256 bits per token
+  const int t0 = (blockIdx.x * (blockDim.x >> 5) + warp) * 4;
+  if (t0 >= a.T) return;
+  const float ninf = -INFINITY;
+  const bool soft = a.gate == 0;
+  float row_m = 0.f, row_inv = 0.f;               // softmax of this lane's token
+  // ------------------------------------------------------------ 1 softmax
+  if (soft) {
+#pragma unroll 1
+    for (int r2 = 0; r2 < 4; r2 += 2) {
+      float4 lv[2][2];
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      const int c = lane + 32 * i;
-      l[i] = c < a.E ? to_f32<L>(row[c]) : -INFINITY;
-      m = fmaxf(m, l[i]);
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          lv[q][i] = make_float4(ninf, ninf, ninf, ninf);
+          if (t0 + r2 + q < a.T && 128 * i < a.E)
+            lv[q][i] = load4<L, VEC>(logits + static_cast<size_t>(t0 + r2 + q) * a.ld,
+                                     4 * lane + 128 * i, a.E);
+        }
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        float* l = reinterpret_cast<float*>(lv[q]);
+        float m = ninf, s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, l[i]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+        if (m == ninf) m = 0.f;                    // no finite logit: all zero
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          l[i] = __expf(l[i] - m);
+          s += l[i];
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int e = 4 * lane + 128 * i;
+          if (e < ROW) *reinterpret_cast<float4*>(rows + (r2 + q) * ROW + e) = lv[q][i];
+        }
+        if (tok == r2 + q) {
+          row_m = m;
+          row_inv = s == 0.f ? 0.f : 1.0f / s;
+        }
+      }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-    if (m == -INFINITY) m = 0.f;
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      p[i] = expf(l[i] - m);
-      s += p[i];
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
-    inv = s > 0.f || !(s == s) ? 1.0f / s : 0.f;
   }
+  seen[lane] = 0u;
+  __syncwarp();
+  // -------------------------------------------------------------- 2 pairs
+  const int t = t0 + tok;
+  int e[kMaxK / 8];
+  float d[kMaxK / 8], sj[kMaxK / 8], v[kMaxK / 8];
+  double D = 0.0, Q = 0.0;
+  bool twice = false;
+  bool some = false;
 #pragma unroll
-  for (int i = 0; i < NB; ++i) buf[lane + 32 * i] = 0.f;
-  float sj = 0.f, slope = 0.f;   // the score and d score / d logit (sigmoid)
-  if (e >= 0) {
-    const float le = to_f32<L>(row[e]);
-    if (a.gate == 0) {
-      sj = expf(le - m) * inv;
-    } else {
-      const float x = expf(-fabsf(le));
-      const float r = 1.0f / (1.0f + x);
-      sj = le >= 0.f ? r : x * r;
-      slope = x * r * r;
+  for (int i = 0; i < kMaxK / 8; ++i) {
+    const int j = sub + 8 * i;
+    e[i] = -1;
+    d[i] = 0.f;
+    sj[i] = 0.f;
+    v[i] = 0.f;
+    if (8 * i >= a.k) continue;
+    if (t < a.T && j < a.k) e[i] = topk_idx[static_cast<size_t>(t) * a.k + j];
+    if (e[i] < 0 || e[i] >= a.E) e[i] = -1;
+    if (e[i] >= 0) {
+      some = true;
+      d[i] = dw[static_cast<size_t>(t) * a.k + j];
+      const float l = to_f32<L>(logits[static_cast<size_t>(t) * a.ld + e[i]]);
+      if (soft) {
+        sj[i] = expf(l - row_m) * row_inv;
+        v[i] = sj[i];                              // d score / d ds
+      } else {
+        const float x = expf(-fabsf(l)), r = 1.0f / (1.0f + x);
+        sj[i] = l >= 0.f ? r : x * r;
+        v[i] = x * r * r;                          // s (1 - s)
+      }
+      const unsigned bit = 1u << (e[i] & 31);
+      twice = twice || (atomicOr(seen + 8 * tok + (e[i] >> 5), bit) & bit);
     }
+    D += sj[i];
+    Q += static_cast<double>(d[i]) * static_cast<double>(sj[i]);
   }
-  double D = sj, Q = static_cast<double>(d) * static_cast<double>(sj);
-  double ds = static_cast<double>(d) * static_cast<double>(a.scale);
+  double f = a.scale, q = 0.0;                     // ds = f (dw - q)
   if (a.norm) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
+    for (int o = 4; o > 0; o >>= 1) {
       D += __shfl_xor_sync(kFull, D, o);
       Q += __shfl_xor_sync(kFull, Q, o);
     }
     D += 1e-9;
-    ds = static_cast<double>(a.scale) * (static_cast<double>(d) * D - Q) / (D * D);
+    f = static_cast<double>(a.scale) / (D * D);
   }
-  if (e < 0) ds = 0.0;
   double dot = 0.0;
-  if (a.gate == 0) {
-    dot = ds * static_cast<double>(sj);
+  float ds[kMaxK / 8];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
+  for (int i = 0; i < kMaxK / 8; ++i) {
+    ds[i] = 0.f;
+    if (8 * i >= a.k || e[i] < 0) continue;
+    q = a.norm ? f * (static_cast<double>(d[i]) * D - Q) : f * static_cast<double>(d[i]);
+    ds[i] = static_cast<float>(q);
+    dot += q * static_cast<double>(sj[i]);
   }
-  __syncwarp();
-  // the same expert twice adds up, in pair order
-  const float v = static_cast<float>(a.gate == 0 ? ds : ds * static_cast<double>(slope));
-  const unsigned same = __match_any_sync(kFull, e);
-  if (__any_sync(kFull, e >= 0 && (same & (same - 1)))) {
-    for (int j = 0; j < a.k; ++j) {
-      if (lane == j && e >= 0) buf[e] += v;
-      __syncwarp();
+  if (soft) {
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
+  }
+  if (__any_sync(kFull, twice)) {
+    // an expert listed twice: the sum of its pairs, in pair order, at each
+    float sum[kMaxK / 8];
+#pragma unroll
+    for (int i = 0; i < kMaxK / 8; ++i) sum[i] = 0.f;
+#pragma unroll
+    for (int ih = 0; ih < kMaxK / 8; ++ih) {
+      if (8 * ih >= a.k) continue;
+      for (int hl = 0; hl < 8; ++hl) {
+        const int eh = __shfl_sync(kFull, e[ih], (tok << 3) | hl);
+        const float dh = __shfl_sync(kFull, ds[ih], (tok << 3) | hl);
+#pragma unroll
+        for (int i = 0; i < kMaxK / 8; ++i)
+          if (eh == e[i]) sum[i] += dh;
+      }
     }
-  } else if (e >= 0) {
-    buf[e] = v;
-  }
-  __syncwarp();
-  L* out = dlogits + static_cast<size_t>(t) * dld;
-  const float fdot = static_cast<float>(dot);
-  const bool chosen = __any_sync(kFull, e >= 0);   // a token without experts: zeros
 #pragma unroll
-  for (int i = 0; i < NB; ++i) {
-    const int c = lane + 32 * i;
-    if (c >= a.E) break;
-    float g = buf[c];
-    if (a.gate == 0) g = chosen ? p[i] * inv * (g - fdot) : 0.f;
-    if constexpr (sizeof(L) == 2)
-      out[c] = __float2bfloat16_rn(g);
-    else
-      out[c] = g;
+    for (int i = 0; i < kMaxK / 8; ++i) ds[i] = sum[i];
+  }
+  const unsigned with = __ballot_sync(kFull, some);
+  const float fdot = soft ? static_cast<float>(dot) : 0.f;
+  // --------------------------------------------------------------- 3 rows
+  const float neg = -fdot * row_inv;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    if (t0 + r >= a.T) break;
+    // a token without experts has a row of zeros, whatever its logits
+    const bool dense = soft && ((with >> (8 * r)) & 0xffu);
+    const float c = __shfl_sync(kFull, neg, 8 * r);
+    L* out = dlogits + static_cast<size_t>(t0 + r) * dld;
+    const float* row = rows + r * ROW;
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int x = 4 * lane + 128 * i;
+        if (x >= a.E) break;
+        float4 g = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (dense) {
+          g = *reinterpret_cast<const float4*>(row + x);
+          g = make_float4(g.x * c, g.y * c, g.z * c, g.w * c);
+        }
+        if constexpr (sizeof(L) == 2) {
+          const __nv_bfloat162 h0 = __floats2bfloat162_rn(g.x, g.y);
+          const __nv_bfloat162 h1 = __floats2bfloat162_rn(g.z, g.w);
+          *reinterpret_cast<uint2*>(out + x) =
+              make_uint2(*reinterpret_cast<const uint32_t*>(&h0),
+                         *reinterpret_cast<const uint32_t*>(&h1));
+        } else {
+          *reinterpret_cast<float4*>(out + x) = g;
+        }
+      }
+    } else {
+      for (int x = lane; x < a.E; x += 32) {
+        const float g = dense ? row[x] * c : 0.f;
+        if constexpr (sizeof(L) == 2) out[x] = __float2bfloat16_rn(g); else out[x] = g;
+      }
+    }
+  }
+  __syncwarp();                                    // the rows before their chosen elements
+#pragma unroll
+  for (int i = 0; i < kMaxK / 8; ++i) {
+    if (8 * i >= a.k || e[i] < 0) continue;
+    L* out = dlogits + static_cast<size_t>(t) * dld + e[i];
+    const float g = v[i] * (ds[i] - fdot);
+    if constexpr (sizeof(L) == 2) *out = __float2bfloat16_rn(g); else *out = g;
   }
 }
 
@@ -575,46 +827,39 @@ template <typename L>
 cudaError_t route_launch(const RouteShape& a, const L* logits, const float* bias,
                          const uint8_t* mask, int32_t* topk_idx, float* topk_w,
                          cudaStream_t stream) {
-  // one warp per block until there are enough tokens for eight on every SM
-  const int warps = a.T <= 148 * 32 ? 1 : 8;
-  const int nb = (a.E + 31) / 32;
+  // one warp per block until there are enough tokens for four on every SM
+  const int warps = a.T <= 148 * 16 ? 1 : kRouteWarps;
   const unsigned grid = static_cast<unsigned>((a.T + 4 * warps - 1) / (4 * warps));
-  const size_t smem = static_cast<size_t>(warps) * 4 * 36 * nb * sizeof(float);
+  const size_t smem = static_cast<size_t>(warps) *
+                      (4 * 36 * ((a.E + 31) / 32) + 8 * kPickRow) * sizeof(float);
+  const bool vec = a.E % 4 == 0 && a.ld % 4 == 0 &&
+                   (reinterpret_cast<uintptr_t>(logits) & (4 * sizeof(L) - 1)) == 0;
+  const int per = a.per;
+  const int total = a.topk_group < a.groups && per % 4 == 0 ? a.topk_group * per : a.E;
   auto go = [&](auto kern) {
     return launch_pdl(kern, dim3(grid), dim3(32 * warps), smem, stream, a, logits, bias, mask,
                       topk_idx, topk_w);
   };
-  switch (nb) {
-    case 1: return go(route_kernel<L, 1>);
-    case 2: return go(route_kernel<L, 2>);
-    case 3: return go(route_kernel<L, 3>);
-    case 4: return go(route_kernel<L, 4>);
-    case 5: return go(route_kernel<L, 5>);
-    case 6: return go(route_kernel<L, 6>);
-    case 7: return go(route_kernel<L, 7>);
-    default: return go(route_kernel<L, 8>);
-  }
+  if (total <= 32) return vec ? go(route_kernel<L, 1, true>) : go(route_kernel<L, 1, false>);
+  if (total <= 64) return vec ? go(route_kernel<L, 2, true>) : go(route_kernel<L, 2, false>);
+  if (total <= 128) return vec ? go(route_kernel<L, 4, true>) : go(route_kernel<L, 4, false>);
+  return vec ? go(route_kernel<L, 8, true>) : go(route_kernel<L, 8, false>);
 }
 
 template <typename L>
 cudaError_t route_bwd_launch(const RouteShape& a, const L* logits, const int32_t* topk_idx,
                              const float* dw, L* dlogits, long long dld, cudaStream_t stream) {
-  const int warps = a.T <= 148 * 8 ? 1 : 8;
-  const unsigned grid = static_cast<unsigned>((a.T + warps - 1) / warps);
-  auto go = [&](auto kern) {
-    return launch_pdl(kern, dim3(grid), dim3(32 * warps), 0, stream, a, logits, topk_idx, dw,
-                      dlogits, dld);
-  };
-  switch ((a.E + 31) / 32) {
-    case 1: return go(route_bwd_kernel<L, 1>);
-    case 2: return go(route_bwd_kernel<L, 2>);
-    case 3: return go(route_bwd_kernel<L, 3>);
-    case 4: return go(route_bwd_kernel<L, 4>);
-    case 5: return go(route_bwd_kernel<L, 5>);
-    case 6: return go(route_bwd_kernel<L, 6>);
-    case 7: return go(route_bwd_kernel<L, 7>);
-    default: return go(route_bwd_kernel<L, 8>);
-  }
+  const int warps = a.T <= 148 * 16 ? 1 : kRouteWarps;
+  const unsigned grid = static_cast<unsigned>((a.T + 4 * warps - 1) / (4 * warps));
+  // the rows of the softmax's exponentials, and the seen bits
+  const size_t smem = static_cast<size_t>(warps) * (4 * ((a.E + 3) & ~3) + 32) * sizeof(float);
+  const uintptr_t align = 4 * sizeof(L) - 1;
+  const bool vec = a.E % 4 == 0 && a.ld % 4 == 0 && dld % 4 == 0 &&
+                   (reinterpret_cast<uintptr_t>(logits) & align) == 0 &&
+                   (reinterpret_cast<uintptr_t>(dlogits) & align) == 0;
+  auto kern = vec ? route_bwd_kernel<L, true> : route_bwd_kernel<L, false>;
+  return launch_pdl(kern, dim3(grid), dim3(32 * warps), smem, stream, a, logits, topk_idx, dw,
+                    dlogits, dld);
 }
 
 }  // namespace
