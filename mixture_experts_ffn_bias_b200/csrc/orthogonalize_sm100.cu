@@ -35,11 +35,12 @@
 //              elements do not average the 11 bits' roundings out (7e-3 seen
 //              on a 1 x 1 matrix), and their products cost next to nothing.
 //
-// The GEMM is persistent over CTA pairs (cluster of two, cta_group::2, tiles
-// of 256 x 256): warp 0 loads (TMA, 128-byte swizzle, a ring of stages), one
-// lane of warp 1 of rank 0 issues the MMAs, warps 2..9 run the epilogue from
-// a double-buffered TMEM accumulator while the next tile's MMAs run.  No
-// load uses cluster multicast; every wait is bounded.
+// The GEMM is persistent: warp 0 loads operand tiles (TMA, 128-byte swizzle, a
+// ring of stages), one lane of warp 1 issues the MMAs, warp 2 moves the added
+// matrix's chunks in and the result's out (TMA, 128 rows x 64 columns), warps
+// 3..10 run the epilogue from a double-buffered TMEM accumulator while the
+// next tile's MMAs run.  No load uses cluster multicast; every wait is
+// bounded.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -64,30 +65,41 @@ constexpr int MODE_POLY = 1;
 constexpr int MODE_APPLY = 2;    // X' as fp16 planes
 constexpr int MODE_LAST = 3;     // the result, in the caller's type and layout
 
-constexpr int TM = 256;          // tile rows (128 per CTA of the pair)
-constexpr int TN = 256;          // tile columns
 constexpr int BK = 64;
-constexpr int OP_BYTES = 128 * BK * 2;    // one CTA's half of an operand tile
-constexpr int STAGE_BYTES = 2 * OP_BYTES;
-constexpr int STAGES = 6;
-constexpr int EPI_WARPS = 8;
-constexpr int NUM_THREADS = 64 + 32 * EPI_WARPS;
 constexpr int CHUNK_KB = 4;               // TERMS 3: k-blocks of an accumulator
-constexpr int TMEM_COLS = 512;            // two accumulators of 256 columns
-constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 + 256;
+constexpr int EPI_WARPS = 8;
+constexpr int NUM_THREADS = 32 * (3 + EPI_WARPS);
+constexpr int PLANE_BYTES = 128 * 64 * 2; // a chunk: 128 rows x 64 columns of fp16
+constexpr int BOX_MN = 64 * 128;          // 64 columns of 64 k-rows, MN-major
+
+// Tile shapes: CG CTAs (1, or a cta_group::2 pair) per tile of 128 CG x TN.
+template <int TERMS, int CG, int TN>
+struct Cfg {
+  static constexpr int TM = 128 * CG;
+  static constexpr int PLANES = TERMS == 3 ? 2 : 1;
+  static constexpr int A_BYTES = 128 * BK * 2;              // one plane, one CTA
+  static constexpr int B_BYTES = TN / CG * BK * 2;
+  static constexpr int STAGE_BYTES = PLANES * (A_BYTES + B_BYTES);
+  static constexpr int EPI_BUFS = STAGE_BYTES >= 65536 ? 1 : 2;
+  static constexpr int EPI_BYTES = EPI_BUFS * 2 * PLANE_BYTES;
+  static constexpr int STAGES_MAX = (232448 - 1280 - EPI_BYTES) / STAGE_BYTES;
+  static constexpr int STAGES = STAGES_MAX > 8 ? 8 : STAGES_MAX;
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_BYTES + 1024 + 256;
+  static constexpr int TMEM_COLS = 2 * TN;                  // two accumulators
+  static_assert(STAGES >= 2 && SMEM_BYTES <= 232448, "shared memory");
+};
 
 struct NsArgs {
   int batch, m, n;
-  int tm, tn;               // tiles of a matrix (gram, poly: tm x tm, upper triangle)
+  int tm, tn;               // tiles of a matrix along its rows and columns
   int tiles;                // tiles of a matrix that are computed
   int kblocks;              // BK-wide blocks of the inner dimension
   float alpha;              // factor of the accumulator
-  float beta;               // factor of the added matrix
-  const __half* add_hi;     // poly: A, apply: X (planes of the output's shape)
-  const __half* add_lo;     // or null
-  long long add_ld, add_bs;
-  __half* out_hi;
-  __half* out_lo;           // or null
+  float beta;               // factor of the added matrix (poly: A, apply: X)
+  int add_planes;           // its planes, 0 for gram
+  int out_planes;           // planes written (not MODE_LAST)
+  __half* out_hi;           // gram, poly: for the mirrored tiles
+  __half* out_lo;
   long long out_ld, out_bs;
   void* out;                // MODE_LAST
   int out_bf16, out_trans;
@@ -100,14 +112,47 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn) {
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, uint64_t* bar,
-                                                 int32_t x, int32_t y, int32_t z) {
+// 3-D tile load into this CTA's shared memory; CG 2: counted on the pair's
+// rank-0 barrier.
+template <int CG>
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int32_t x, int32_t y, int32_t z) {
+  if constexpr (CG == 2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];"
+        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32_rank0(bar)),
+          "r"(x), "r"(y), "r"(z)
+        : "memory");
+  } else {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];"
+        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)),
+          "r"(x), "r"(y), "r"(z)
+        : "memory");
+  }
+}
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int32_t x,
+                                             int32_t y, int32_t z) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];"
-      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32_rank0(bar)),
-        "r"(x), "r"(y), "r"(z)
+      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];"
+      ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
       : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                    uint32_t accumulate) {
+  if constexpr (CG == 2)
+    tc_mma_f16_pair(d, a, b, idesc, accumulate);
+  else
+    tc_mma_f16(d, a, b, idesc, accumulate);
+}
+template <int CG>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if constexpr (CG == 2) tc_commit_pair(bar); else tc_commit(bar);
 }
 
 __device__ __forceinline__ uint32_t half2_bits(__half a, __half b) {
@@ -115,112 +160,133 @@ __device__ __forceinline__ uint32_t half2_bits(__half a, __half b) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
-// Tile t of a matrix: (i, j), for the symmetric products of the upper
-// triangle (j >= i), row by row.
-template <int MODE>
+// Tile t of a matrix: rows i, columns j.  The symmetric products compute the
+// tiles that reach the diagonal or lie above it, j >= i TM / TN, row by row.
+template <int MODE, int RATIO>
 __device__ __forceinline__ void tile_of(const NsArgs& a, int t, int& i, int& j) {
   if (MODE == MODE_GRAM || MODE == MODE_POLY) {
     i = 0;
-    while (t >= a.tm - i) {
-      t -= a.tm - i;
+    while (t >= a.tn - RATIO * i) {
+      t -= a.tn - RATIO * i;
       ++i;
     }
-    j = i + t;
+    j = RATIO * i + t;
   } else {
     i = t / a.tn;
     j = t - i * a.tn;
   }
 }
 
-// 32 values of one accumulator row, columns c0 .. c0 + 31 of the tile's row r:
-// the added matrix's part and the stores.
+// 16-byte piece c (0..7) of a chunk's row, 128-byte swizzle.
+__device__ __forceinline__ uint4* piece(uint8_t* plane, int row, int c) {
+  return reinterpret_cast<uint4*>(plane + row * 128 + ((c ^ (row & 7)) << 4));
+}
+
+// 32 accumulator values of tile row `row` (matrix row r), columns c0 .. c0 + 31
+// of the matrix: the added planes' part, read from the chunk buffer, and the
+// result's planes, left in their place there.  `half`: which 32 columns of
+// the chunk.
 template <int MODE>
-__device__ __forceinline__ void finish32(const NsArgs& a, const float (&acc)[32], int b, int r,
-                                         int c0, bool mirror, int lane) {
+__device__ __forceinline__ void finish32(const NsArgs& a, const float (&acc)[32], uint8_t* buf,
+                                         int b, int row, int r, int c0, int half, bool mirror,
+                                         int lane) {
   float v[32];
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = a.alpha * acc[i];
-  const bool row_ok = r < a.m;
   if (MODE != MODE_GRAM) {
-    if (row_ok) {
-      const size_t at = static_cast<size_t>(b) * a.add_bs + static_cast<size_t>(r) * a.add_ld + c0;
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const __half* src = p == 0 ? a.add_hi : a.add_lo;
-        if (src == nullptr) continue;
+    for (int p = 0; p < 2; ++p) {
+      if (p >= a.add_planes) break;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (c0 + 8 * i >= a.add_ld) break;
-          const uint4 q = *reinterpret_cast<const uint4*>(src + at + 8 * i);
-          const __half2* h = reinterpret_cast<const __half2*>(&q);
+      for (int i = 0; i < 4; ++i) {
+        const uint4 q = *piece(buf + p * PLANE_BYTES, row, half * 4 + i);
+        const __half2* h = reinterpret_cast<const __half2*>(&q);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = __half22float2(h[e]);
-            v[8 * i + 2 * e] = fmaf(a.beta, f.x, v[8 * i + 2 * e]);
-            v[8 * i + 2 * e + 1] = fmaf(a.beta, f.y, v[8 * i + 2 * e + 1]);
-          }
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = __half22float2(h[e]);
+          v[8 * i + 2 * e] = fmaf(a.beta, f.x, v[8 * i + 2 * e]);
+          v[8 * i + 2 * e + 1] = fmaf(a.beta, f.y, v[8 * i + 2 * e + 1]);
         }
       }
     }
   }
   if (MODE == MODE_LAST) {
-    // the caller's rows and columns: X[r][c] is out[r][c], or out[c][r]
-    if (!row_ok) return;
     const size_t base = static_cast<size_t>(b) * a.o_bs;
-    const int nc = a.n - c0 < 32 ? a.n - c0 : 32;
-    if (a.out_bf16) {
-      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + base;
-      if (a.out_trans) {
+    if (a.out_trans) {
+      // X[r][c] is out[c][r]: neighbouring lanes store neighbouring elements
+      if (r >= a.m) return;
+      const int nc = a.n - c0 < 32 ? a.n - c0 : 32;
+      if (a.out_bf16) {
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + base;
 #pragma unroll
         for (int i = 0; i < 32; ++i)
           if (i < nc) o[static_cast<size_t>(c0 + i) * a.o_ld + r] = __float2bfloat16_rn(v[i]);
       } else {
-        __nv_bfloat16* p = o + static_cast<size_t>(r) * a.o_ld + c0;
-        if (nc == 32 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint4 q;
-            uint32_t* w = reinterpret_cast<uint32_t*>(&q);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              __nv_bfloat162 h = __floats2bfloat162_rn(v[8 * i + 2 * e], v[8 * i + 2 * e + 1]);
-              w[e] = *reinterpret_cast<uint32_t*>(&h);
-            }
-            reinterpret_cast<uint4*>(p)[i] = q;
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (i < nc) p[i] = __float2bfloat16_rn(v[i]);
-        }
-      }
-    } else {
-      float* o = static_cast<float*>(a.out) + base;
-      if (a.out_trans) {
+        float* o = static_cast<float*>(a.out) + base;
 #pragma unroll
         for (int i = 0; i < 32; ++i)
           if (i < nc) o[static_cast<size_t>(c0 + i) * a.o_ld + r] = v[i];
-      } else {
-        float* p = o + static_cast<size_t>(r) * a.o_ld + c0;
-        if (nc == 32 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+      }
+      return;
+    }
+    // staged in the chunk (fp32: columns 0-15 in the first plane's place,
+    // 16-31 in the second's), then stored along the rows
+    const int row0 = row - lane, r0 = r - lane;
+    if (a.out_bf16) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            reinterpret_cast<float4*>(p)[i] =
-                make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-        } else {
+      for (int i = 0; i < 4; ++i) {
+        uint32_t w[4];
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (i < nc) p[i] = v[i];
+        for (int e = 0; e < 4; ++e) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(v[8 * i + 2 * e], v[8 * i + 2 * e + 1]);
+          w[e] = *reinterpret_cast<const uint32_t*>(&h);
         }
+        *piece(buf, row, half * 4 + i) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      __syncwarp();
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + base + c0;
+      if (c0 + 32 <= a.n && a.o_ld % 8 == 0 && (reinterpret_cast<uintptr_t>(o) & 15) == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int y = 8 * i + (lane >> 2);
+          if (r0 + y < a.m)
+            *reinterpret_cast<uint4*>(o + static_cast<size_t>(r0 + y) * a.o_ld + (lane & 3) * 8) =
+                *piece(buf, row0 + y, half * 4 + (lane & 3));
+        }
+      } else if (c0 + lane < a.n) {
+        for (int y = 0; y < 32 && r0 + y < a.m; ++y)
+          o[static_cast<size_t>(r0 + y) * a.o_ld + lane] =
+              reinterpret_cast<const __nv_bfloat16*>(
+                  piece(buf, row0 + y, half * 4 + (lane >> 3)))[lane & 7];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        *piece(buf + (i >> 2) * PLANE_BYTES, row, half * 4 + (i & 3)) =
+            make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                       __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
+      __syncwarp();
+      float* o = static_cast<float*>(a.out) + base + c0;
+      if (c0 + 32 <= a.n && a.o_ld % 4 == 0 && (reinterpret_cast<uintptr_t>(o) & 15) == 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int y = 4 * i + (lane >> 3), c = lane & 7;
+          if (r0 + y < a.m)
+            *reinterpret_cast<uint4*>(o + static_cast<size_t>(r0 + y) * a.o_ld + c * 4) =
+                *piece(buf + (c >> 2) * PLANE_BYTES, row0 + y, half * 4 + (c & 3));
+        }
+      } else if (c0 + lane < a.n) {
+        for (int y = 0; y < 32 && r0 + y < a.m; ++y)
+          o[static_cast<size_t>(r0 + y) * a.o_ld + lane] = reinterpret_cast<const float*>(
+              piece(buf + (lane >> 4) * PLANE_BYTES, row0 + y,
+                    half * 4 + ((lane >> 2) & 3)))[lane & 3];
       }
     }
     return;
   }
-  const size_t obase = static_cast<size_t>(b) * a.out_bs;
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
-    __half* plane = p == 0 ? a.out_hi : a.out_lo;
-    if (plane == nullptr) break;
+    if (p >= a.out_planes) break;
     uint32_t w[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -231,18 +297,15 @@ __device__ __forceinline__ void finish32(const NsArgs& a, const float (&acc)[32]
         v[2 * i + 1] -= __half2float(h1);
       }
     }
-    if (row_ok) {
-      __half* dst = plane + obase + static_cast<size_t>(r) * a.out_ld + c0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (c0 + 8 * i < a.out_ld)
-          reinterpret_cast<uint4*>(dst)[i] =
-              make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-    }
+    for (int i = 0; i < 4; ++i)
+      *piece(buf + p * PLANE_BYTES, row, half * 4 + i) =
+          make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     if (MODE == MODE_GRAM || MODE == MODE_POLY) {
       if (mirror) {
-        // the mirrored tile: two lanes exchange a column pair, so that each
-        // stores two neighbouring rows' values of one column
+        // the mirrored tile, straight to memory: two lanes exchange a column
+        // pair, so that each stores two neighbouring rows' values of one column
+        __half* plane = (p == 0 ? a.out_hi : a.out_lo) + static_cast<size_t>(b) * a.out_bs;
         const int odd = lane & 1;
         const int rr = r - odd;              // even, and out_ld is a multiple of 64
 #pragma unroll
@@ -252,39 +315,46 @@ __device__ __forceinline__ void finish32(const NsArgs& a, const float (&acc)[32]
                                   : __byte_perm(w[i], other, 0x5410);
           const int c = c0 + 2 * i + odd;
           if (c < a.m && rr < a.m)
-            *reinterpret_cast<uint32_t*>(plane + obase + static_cast<size_t>(c) * a.out_ld + rr) =
-                st;
+            *reinterpret_cast<uint32_t*>(plane + static_cast<size_t>(c) * a.out_ld + rr) = st;
         }
       }
     }
   }
 }
 
-template <int MODE, int TERMS>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
-ns_gemm_kernel(const __grid_constant__ CUtensorMap a_hi, const __grid_constant__ CUtensorMap a_lo,
-               const __grid_constant__ CUtensorMap b_hi, const __grid_constant__ CUtensorMap b_lo,
-               const NsArgs args) {
+// a_*, b_*: the operands' planes; add_*: the added matrix, out_*: the result,
+// both in chunks of 128 rows x 64 columns.
+struct NsMaps {
+  CUtensorMap a[2], b[2], add[2], out[2];
+};
+
+template <int MODE, int TERMS, int CG, int TN>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+ns_gemm_kernel(const __grid_constant__ NsMaps maps, const NsArgs args) {
+  using C = Cfg<TERMS, CG, TN>;
+  constexpr int STAGES = C::STAGES;
+  constexpr int RATIO = C::TM / TN;
   constexpr bool BMN = MODE == MODE_APPLY || MODE == MODE_LAST;
-  constexpr uint32_t IDESC = idesc_f16_f32(TM, TN, BMN);
-  constexpr int BOX_MN = 64 * 128;   // 64 columns of 64 k-rows
+  constexpr uint32_t IDESC = idesc_f16_f32(C::TM, TN, BMN);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint8_t* sA = smem;
-  uint8_t* sB = smem + STAGES * OP_BYTES;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_BYTES);
-  uint64_t* full_bar = bars;                      // rank 0's copy is used
+  uint8_t* sEpi = smem + STAGES * C::STAGE_BYTES;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sEpi + C::EPI_BYTES);
+  uint64_t* full_bar = bars;                      // CG 2: rank 0's copy is used
   uint64_t* empty_bar = bars + STAGES;            // both copies
   uint64_t* tfull_bar = bars + 2 * STAGES;        // both copies
   uint64_t* tempty_bar = bars + 2 * STAGES + 2;   // rank 0's copy
-  uint64_t* drain_bar = bars + 2 * STAGES + 4;
+  uint64_t* ready_bar = bars + 2 * STAGES + 4;    // a chunk buffer may be used
+  uint64_t* done_bar = bars + 2 * STAGES + 6;     // and has been
+  uint64_t* drain_bar = bars + 2 * STAGES + 8;
   __shared__ uint32_t s_tmem_base;
   __shared__ int s_abort;
 
+  pdl_trigger();   // the grid is resident at once: the next kernel may set up
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
-  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
+  const int unit = blockIdx.x / CG, units = gridDim.x / CG;
   const long long total = static_cast<long long>(args.batch) * args.tiles;
   const int chunk_kb = TERMS == 3 ? CHUNK_KB : args.kblocks;
 
@@ -296,27 +366,32 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap a_hi, const __grid_constant__
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull_bar[i], 1);
-      mbar_init(&tempty_bar[i], 2 * EPI_WARPS);
+      mbar_init(&tempty_bar[i], CG * EPI_WARPS);
+      mbar_init(&ready_bar[i], 1);
+      mbar_init(&done_bar[i], EPI_WARPS);
     }
     mbar_init(drain_bar, 1);
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&a_hi);
-    tma_prefetch_desc(&b_hi);
-    if (TERMS == 3) {
-      tma_prefetch_desc(&a_lo);
-      tma_prefetch_desc(&b_lo);
+    for (int p = 0; p < C::PLANES; ++p) {
+      tma_prefetch_desc(&maps.a[p]);
+      tma_prefetch_desc(&maps.b[p]);
     }
   }
   if (warp == 1) {
-    tmem_alloc_pair(&s_tmem_base, TMEM_COLS);
-    tmem_relinquish_pair();
+    if constexpr (CG == 2) {
+      tmem_alloc_pair(&s_tmem_base, C::TMEM_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(&s_tmem_base, C::TMEM_COLS);
+      tmem_relinquish();
+    }
   }
   pdl_wait();   // everything above touches no global memory
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();
+  if constexpr (CG == 2) cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem_base = s_tmem_base;
   volatile int* abort_flag = &s_abort;
@@ -327,40 +402,38 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap a_hi, const __grid_constant__
       int stage = 0;
       uint32_t phase = 0, issued_mask = 0, issued_phase = 0;
       bool ok = true;
-      for (long long t = pair; t < total && ok; t += npairs) {
+      for (long long t = unit; t < total && ok; t += units) {
         const int b = static_cast<int>(t / args.tiles);
         int ti, tj;
-        tile_of<MODE>(args, static_cast<int>(t - static_cast<long long>(b) * args.tiles), ti, tj);
-        const int arow = ti * TM + static_cast<int>(rank) * 128;
-        const int bcol = tj * TN + static_cast<int>(rank) * 128;
-        for (int k0 = 0; k0 < args.kblocks && ok; k0 += chunk_kb) {
-          const int k1 = min(k0 + chunk_kb, args.kblocks);
-          // TERMS 3: hi lo, lo hi, hi hi (the small products first)
-          for (int term = TERMS == 3 ? 0 : 2; term < 3 && ok; ++term) {
-            const CUtensorMap* ma = term == 1 ? &a_lo : &a_hi;
-            const CUtensorMap* mb = term == 0 ? &b_lo : &b_hi;
-            for (int kb = k0; kb < k1; ++kb) {
-              if (!mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag)) { ok = false; break; }
-              if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], 2 * STAGE_BYTES);
-              const int k = kb * BK;
-              tma_load_3d_pair(sA + stage * OP_BYTES, ma, &full_bar[stage], k, arow, b);
-              if (BMN) {
-                tma_load_3d_pair(sB + stage * OP_BYTES, mb, &full_bar[stage], bcol, k, b);
-                tma_load_3d_pair(sB + stage * OP_BYTES + BOX_MN, mb, &full_bar[stage], bcol + 64,
-                                 k, b);
-              } else {
-                tma_load_3d_pair(sB + stage * OP_BYTES, mb, &full_bar[stage], k, bcol, b);
-              }
-              issued_mask |= 1u << stage;
-              issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
-              if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        tile_of<MODE, RATIO>(args, static_cast<int>(t - static_cast<long long>(b) * args.tiles),
+                             ti, tj);
+        const int arow = ti * C::TM + static_cast<int>(rank) * 128;
+        const int bcol = tj * TN + static_cast<int>(rank) * (TN / CG);
+        for (int kb = 0; kb < args.kblocks; ++kb) {
+          if (!mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag)) { ok = false; break; }
+          if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], CG * C::STAGE_BYTES);
+          uint8_t* sA = smem + stage * C::STAGE_BYTES;
+          uint8_t* sB = sA + C::PLANES * C::A_BYTES;
+          const int k = kb * BK;
+#pragma unroll
+          for (int p = 0; p < C::PLANES; ++p) {
+            tma_load_3d<CG>(sA + p * C::A_BYTES, &maps.a[p], &full_bar[stage], k, arow, b);
+            if (BMN) {
+#pragma unroll
+              for (int x = 0; x < TN / CG; x += 64)
+                tma_load_3d<CG>(sB + p * C::B_BYTES + (x / 64) * BOX_MN, &maps.b[p],
+                                &full_bar[stage], bcol + x, k, b);
+            } else {
+              tma_load_3d<CG>(sB + p * C::B_BYTES, &maps.b[p], &full_bar[stage], k, bcol, b);
             }
           }
+          issued_mask |= 1u << stage;
+          issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
       }
-      pdl_trigger();   // all loads issued: the next kernel may launch
       if (!ok && rank == 0) {
-        // rank 0's stage barriers count both CTAs' copies: let them all land
+        // (CG 2: rank 0's stage barriers count both CTAs' copies) let them land
         for (int s = 0; s < STAGES; ++s) {
           if (!(issued_mask & (1u << s))) continue;
           const uint32_t par = (issued_phase >> s) & 1u;
@@ -376,117 +449,203 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap a_hi, const __grid_constant__
       int stage = 0, it = 0;
       uint32_t phase = 0;
       bool ok = true, issued_any = false;
-      for (long long t = pair; t < total && ok; t += npairs) {
+      for (long long t = unit; t < total && ok; t += units) {
         for (int k0 = 0; k0 < args.kblocks && ok; k0 += chunk_kb, ++it) {
-          const int nkb = TERMS * (min(k0 + chunk_kb, args.kblocks) - k0);
+          const int k1 = min(k0 + chunk_kb, args.kblocks);
           const int acc = it & 1;
           if (!mbar_wait(&tempty_bar[acc], ((it >> 1) & 1) ^ 1u, abort_flag)) { ok = false; break; }
           tc_fence_after();
           const uint32_t d_tmem = tmem_base + acc * TN;
-          for (int kb = 0; kb < nkb; ++kb) {
+          for (int kb = k0; kb < k1; ++kb) {
             if (!mbar_wait(&full_bar[stage], phase, abort_flag)) { ok = false; break; }
             tc_fence_after();
-            const uint32_t a_addr = smem_u32(sA + stage * OP_BYTES);
-            const uint32_t b_addr = smem_u32(sB + stage * OP_BYTES);
+            const uint32_t a_addr = smem_u32(smem + stage * C::STAGE_BYTES);
+            const uint32_t b_addr = a_addr + C::PLANES * C::A_BYTES;
+            // TERMS 3: hi lo, lo hi, hi hi (the small products first)
 #pragma unroll
-            for (int kk = 0; kk < BK / 16; ++kk) {
-              const uint64_t bd = BMN ? smem_desc_sw128_mn(b_addr + kk * 16 * 128, BOX_MN)
-                                      : smem_desc_sw128(b_addr + kk * 32);
-              tc_mma_f16_pair(d_tmem, smem_desc_sw128(a_addr + kk * 32), bd, IDESC,
-                              (kb | kk) != 0 ? 1u : 0u);
+            for (int term = 3 - TERMS; term < 3; ++term) {
+              const uint32_t at = a_addr + (TERMS == 3 && term == 1 ? C::A_BYTES : 0);
+              const uint32_t bt = b_addr + (TERMS == 3 && term == 0 ? C::B_BYTES : 0);
+#pragma unroll
+              for (int kk = 0; kk < BK / 16; ++kk) {
+                const uint64_t bd = BMN ? smem_desc_sw128_mn(bt + kk * 16 * 128, BOX_MN)
+                                        : smem_desc_sw128(bt + kk * 32);
+                mma<CG>(d_tmem, smem_desc_sw128(at + kk * 32), bd, IDESC,
+                        (kb != k0 || kk != 0 || term != 3 - TERMS) ? 1u : 0u);
+              }
             }
             issued_any = true;
-            tc_commit_pair(&empty_bar[stage]);
+            commit<CG>(&empty_bar[stage]);
             if (++stage == STAGES) { stage = 0; phase ^= 1u; }
           }
           if (!ok) break;
-          tc_commit_pair(&tfull_bar[acc]);
+          commit<CG>(&tfull_bar[acc]);
         }
       }
       if (!ok && issued_any) {
-        tc_commit_pair(drain_bar);
+        commit<CG>(drain_bar);
         const unsigned long long t0 = globaltimer_ns();
         while (!mbar_try_wait(drain_bar, 0))
           if (globaltimer_ns() - t0 > kWaitLimitNs) break;
       }
     }
+  } else if (warp == 2) {
+    // ------------- mover: the added matrix's chunks in, the result's chunks out
+    if (lane == 0) {
+      long long in_t = unit;       // the next chunk to make ready
+      int in_c = 0;
+      auto make_ready = [&](int buf) {
+        if (in_t >= total) return;
+        const int b = static_cast<int>(in_t / args.tiles);
+        int ti, tj;
+        tile_of<MODE, RATIO>(
+            args, static_cast<int>(in_t - static_cast<long long>(b) * args.tiles), ti, tj);
+        if (MODE == MODE_GRAM) {
+          mbar_arrive(&ready_bar[buf]);
+        } else {
+          mbar_arrive_expect_tx(&ready_bar[buf], args.add_planes * PLANE_BYTES);
+          for (int p = 0; p < args.add_planes; ++p)
+            tma_load_3d<1>(sEpi + (buf * 2 + p) * PLANE_BYTES, &maps.add[p], &ready_bar[buf],
+                           tj * TN + in_c * 64, ti * C::TM + static_cast<int>(rank) * 128, b);
+        }
+        if (++in_c == TN / 64) {
+          in_c = 0;
+          in_t += units;
+        }
+      };
+      for (int i = 0; i < C::EPI_BUFS; ++i) make_ready(i);
+      bool ok = true;
+      int s = 0;
+      for (long long t = unit; t < total && ok; t += units) {
+        const int b = static_cast<int>(t / args.tiles);
+        int ti, tj;
+        tile_of<MODE, RATIO>(args, static_cast<int>(t - static_cast<long long>(b) * args.tiles),
+                             ti, tj);
+        const int ncols = BMN ? args.n : args.m;
+        for (int c = 0; c < TN / 64; ++c, ++s) {
+          const int buf = s % C::EPI_BUFS;
+          if (!mbar_wait(&done_bar[buf], (s / C::EPI_BUFS) & 1, abort_flag)) { ok = false; break; }
+          const int row = ti * C::TM + static_cast<int>(rank) * 128, col = tj * TN + c * 64;
+          if (MODE != MODE_LAST && row < args.m && col < ncols) {
+            for (int p = 0; p < args.out_planes; ++p)
+              tma_store_3d(&maps.out[p], sEpi + (buf * 2 + p) * PLANE_BYTES, col, row, b);
+            bulk_commit();
+            bulk_wait_read_all();   // the buffer may be written again
+          }
+          make_ready(buf);
+        }
+      }
+      bulk_wait_all();
+      if (!ok && MODE != MODE_GRAM) {
+        // let the chunk loads in flight land
+        for (int i = 0; i < C::EPI_BUFS; ++i) {
+          const unsigned long long t0 = globaltimer_ns();
+          const uint32_t par = ((s + ((i - s % C::EPI_BUFS) + C::EPI_BUFS) % C::EPI_BUFS) /
+                                C::EPI_BUFS) & 1;
+          while (!mbar_try_wait(&ready_bar[i], par))
+            if (globaltimer_ns() - t0 > kWaitLimitNs) break;
+        }
+      }
+    }
   } else {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;              // the TMEM lanes this warp may read
-    const int half = (warp - 2) >> 2;    // and its 128 of the 256 columns
-    int it = 0;
+    const int half = (warp - 3) >> 2;    // and its 32 columns of every 64
+    const int row = q * 32 + lane;
+    const uint32_t lane_addr = (static_cast<uint32_t>(q * 32) << 16) + half * 32;
+    int it = 0, s = 0;
     bool ok = true;
-    for (long long t = pair; t < total && ok; t += npairs) {
+    auto wait = [&](uint64_t* bar, uint32_t par) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, par, abort_flag));
+    };
+    auto release = [&](uint64_t* bar) {   // an accumulator, to rank 0's issuer
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (CG == 2) mbar_arrive_rank0(bar); else mbar_arrive(bar);
+      }
+    };
+    for (long long t = unit; t < total && ok; t += units) {
       const int b = static_cast<int>(t / args.tiles);
       int ti, tj;
-      tile_of<MODE>(args, static_cast<int>(t - static_cast<long long>(b) * args.tiles), ti, tj);
-      const int warp_r0 = ti * TM + static_cast<int>(rank) * 128 + q * 32;
-      const int c0 = tj * TN + half * 128;
-      const int ncols = (MODE == MODE_GRAM || MODE == MODE_POLY) ? args.m : args.n;
-      const uint32_t lane_addr = (static_cast<uint32_t>(q * 32) << 16) + half * 128;
+      tile_of<MODE, RATIO>(args, static_cast<int>(t - static_cast<long long>(b) * args.tiles), ti,
+                           tj);
+      const int r = ti * C::TM + static_cast<int>(rank) * 128 + row;
+      const bool mirror = tj >= RATIO * (ti + 1);
+      // one chunk: its buffer, the 32 sums, and the hand-over to the mover
+      auto chunk = [&](int c, const float (&f)[32]) {
+        const int buf = s % C::EPI_BUFS;
+        if (!wait(&ready_bar[buf], (s / C::EPI_BUFS) & 1)) return false;
+        finish32<MODE>(args, f, sEpi + buf * 2 * PLANE_BYTES, b, row, r, tj * TN + c * 64 + half * 32,
+                       half, mirror, lane);
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&done_bar[buf]);
+        ++s;
+        return true;
+      };
       if constexpr (TERMS == 1) {
         const int acc = it & 1;
-        ok = __all_sync(0xffffffffu, mbar_wait(&tfull_bar[acc], (it >> 1) & 1, abort_flag));
+        ok = wait(&tfull_bar[acc], (it >> 1) & 1);
         if (!ok) break;
         ++it;
         tc_fence_after();
-        const uint32_t t_addr = tmem_base + acc * TN + lane_addr;
 #pragma unroll 1
-        for (int c = 0; c < 128; c += 32) {
-          if (warp_r0 >= args.m || c0 + c >= ncols) break;   // warp-uniform
+        for (int c = 0; c < TN / 64 && ok; ++c) {
           uint32_t v[32];
-          tmem_ld16(t_addr + c, *reinterpret_cast<uint32_t(*)[16]>(&v[0]));
-          tmem_ld16(t_addr + c + 16, *reinterpret_cast<uint32_t(*)[16]>(&v[16]));
+          const uint32_t t_addr = tmem_base + acc * TN + lane_addr + c * 64;
+          tmem_ld16(t_addr, *reinterpret_cast<uint32_t(*)[16]>(&v[0]));
+          tmem_ld16(t_addr + 16, *reinterpret_cast<uint32_t(*)[16]>(&v[16]));
           tmem_ld_wait();
+          if (c + 1 == TN / 64) release(&tempty_bar[acc]);
           float f[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
-          finish32<MODE>(args, f, b, warp_r0 + lane, c0 + c, ti != tj, lane);
+          ok = chunk(c, f);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_rank0(&tempty_bar[acc]);
       } else {
-        // the chunks' accumulators, added in fp32
-        float sum[128];
+        // the accumulators of CHUNK_KB k-blocks, added in fp32
+        float sum[TN / 64][32];
 #pragma unroll
-        for (int i = 0; i < 128; ++i) sum[i] = 0.f;
+        for (int c = 0; c < TN / 64; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sum[c][i] = 0.f;
         for (int k0 = 0; k0 < args.kblocks; k0 += chunk_kb, ++it) {
           const int acc = it & 1;
-          ok = __all_sync(0xffffffffu, mbar_wait(&tfull_bar[acc], (it >> 1) & 1, abort_flag));
+          ok = wait(&tfull_bar[acc], (it >> 1) & 1);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t t_addr = tmem_base + acc * TN + lane_addr;
 #pragma unroll
-          for (int c = 0; c < 128; c += 16) {
-            uint32_t v[16];
-            tmem_ld16(t_addr + c, v);
-            tmem_ld_wait();
+          for (int c = 0; c < TN / 64; ++c)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) sum[c + i] += __uint_as_float(v[i]);
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_rank0(&tempty_bar[acc]);
+            for (int h = 0; h < 2; ++h) {
+              uint32_t v[16];
+              tmem_ld16(tmem_base + acc * TN + lane_addr + c * 64 + 16 * h, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) sum[c][16 * h + i] += __uint_as_float(v[i]);
+            }
+          release(&tempty_bar[acc]);
         }
         if (!ok) break;
 #pragma unroll
-        for (int c = 0; c < 128; c += 32)
-          if (warp_r0 < args.m && c0 + c < ncols)
-            finish32<MODE>(args, *reinterpret_cast<const float(*)[32]>(&sum[c]), b,
-                           warp_r0 + lane, c0 + c, ti != tj, lane);
+        for (int c = 0; c < TN / 64; ++c)
+          if (ok) ok = chunk(c, sum[c]);
       }
     }
   }
 
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();        // neither CTA leaves while the other still uses the pair
+  if constexpr (CG == 2) cluster_sync_all();   // neither CTA leaves the other early
   if (threadIdx.x == 0 && s_abort) atomicOr(args.status, kDevTimeout);
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc_pair(tmem_base, TMEM_COLS);
+    if constexpr (CG == 2)
+      tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+    else
+      tmem_dealloc(tmem_base, C::TMEM_COLS);
   }
 }
 
@@ -650,25 +809,46 @@ int num_sms() {
   return n > 0 ? n : 148;
 }
 
-template <int MODE, int TERMS>
-cudaError_t launch_ns(const CUtensorMap& ah, const CUtensorMap& al, const CUtensorMap& bh,
-                      const CUtensorMap& bl, const NsArgs& args, cudaStream_t stream) {
-  auto kern = ns_gemm_kernel<MODE, TERMS>;
+template <int MODE, int TERMS, int CG, int TN>
+cudaError_t launch_ns(const NsMaps& maps, NsArgs args, cudaStream_t stream) {
+  using C = Cfg<TERMS, CG, TN>;
+  auto kern = ns_gemm_kernel<MODE, TERMS, CG, TN>;
   static std::atomic<unsigned long long> attr_done{0};
   int dev = 0;
   cudaGetDevice(&dev);
   const unsigned long long bit = 1ull << (dev & 63);
   if (!(attr_done.load(std::memory_order_acquire) & bit)) {
     cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
     if (e != cudaSuccess) return e;
     attr_done.fetch_or(bit, std::memory_order_acq_rel);
   }
+  constexpr bool SYM = MODE == MODE_GRAM || MODE == MODE_POLY;
+  args.tm = (args.m + C::TM - 1) / C::TM;
+  args.tn = ((SYM ? args.m : args.n) + TN - 1) / TN;
+  args.tiles = 0;
+  if (SYM)
+    for (int i = 0; i < args.tm; ++i) args.tiles += args.tn - C::TM / TN * i;
+  else
+    args.tiles = args.tm * args.tn;
   const long long total = static_cast<long long>(args.batch) * args.tiles;
-  const int max_pairs = num_sms() / 2;
-  const int pairs = static_cast<int>(total < max_pairs ? total : max_pairs);
-  return launch_pdl(kern, dim3(2 * pairs), dim3(NUM_THREADS), SMEM_BYTES, stream, ah, al, bh, bl,
-                    args);
+  const int max_units = num_sms() / CG;
+  const int units = static_cast<int>(total < max_units ? total : max_units);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(CG * units);
+  cfg.blockDim = dim3(NUM_THREADS);
+  cfg.dynamicSmemBytes = C::SMEM_BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CG;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, maps, args);
 }
 
 inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -677,6 +857,12 @@ inline long long pad64(int v) { return (static_cast<long long>(v) + 63) / 64 * 6
 // Products of three terms (pairs of planes) or of the high planes alone.
 bool three_terms(const OrthoShape& s) {
   return !s.out_bf16 || (s.rows < s.cols ? s.rows : s.cols) < 64;
+}
+
+// Tiles of 128 x 64 on single CTAs instead of 256 x 256 on pairs.
+bool small_tiles(int batch, int m, int n) {
+  const long long big = static_cast<long long>(batch) * ((m + 255) / 256) * ((n + 255) / 256);
+  return big < 74;
 }
 
 struct OrthoLayout {
@@ -709,7 +895,8 @@ OrthoLayout ortho_layout(const OrthoShape& s) {
   return L;
 }
 
-template <int TERMS>
+// The steps with tiles of 128 CG x TN.
+template <int TERMS, int CG, int TN>
 cudaError_t run_steps(const OrthoShape& s, void* out, void* ws, cudaStream_t stream) {
   const OrthoLayout L = ortho_layout(s);
   uint8_t* w = static_cast<uint8_t*>(ws);
@@ -721,64 +908,79 @@ cudaError_t run_steps(const OrthoShape& s, void* out, void* ws, cudaStream_t str
   __half* al = TERMS == 3 ? reinterpret_cast<__half*>(w + L.al) : nullptr;
   __half* bh = reinterpret_cast<__half*>(w + L.bh);
   __half* bl = TERMS == 3 ? reinterpret_cast<__half*>(w + L.bl) : nullptr;
-  CUtensorMap xk[2][2], xn[2][2], ma[2], mb[2];   // [buffer][plane]
+  // maps by box rows: 128 (A operand, chunks), TN / CG (B operand, K-major),
+  // BK (X as the B operand of the apply product, MN-major)
+  CUtensorMap x128[2][2], xb[2][2], xk[2][2], a128[2], ab[2], b128[2];   // [buffer][plane]
   for (int i = 0; i < 2; ++i)
     for (int p = 0; p < 2; ++p) {
       const void* base = w + (p ? L.xl[i] : L.xh[i]);
-      if (!make_map3(&xk[i][p], base, m, n, ldx, s.batch, bsx, 128) ||
-          !make_map3(&xn[i][p], base, m, n, ldx, s.batch, bsx, BK))
+      if (!make_map3(&x128[i][p], base, m, n, ldx, s.batch, bsx, 128) ||
+          !make_map3(&xb[i][p], base, m, n, ldx, s.batch, bsx, TN / CG) ||
+          !make_map3(&xk[i][p], base, m, n, ldx, s.batch, bsx, BK))
         return cudaErrorInvalidValue;
     }
   for (int p = 0; p < 2; ++p)
-    if (!make_map3(&ma[p], p && al ? al : ah, m, m, lda, s.batch, bsa, 128) ||
-        !make_map3(&mb[p], p && bl ? bl : bh, m, m, lda, s.batch, bsa, 128))
+    if (!make_map3(&a128[p], p && al ? al : ah, m, m, lda, s.batch, bsa, 128) ||
+        !make_map3(&ab[p], p && al ? al : ah, m, m, lda, s.batch, bsa, TN / CG) ||
+        !make_map3(&b128[p], p && bl ? bl : bh, m, m, lda, s.batch, bsa, 128))
       return cudaErrorInvalidValue;
-  const int tm = (m + TM - 1) / TM, tn = (n + TN - 1) / TN;
   NsArgs base{};
   base.batch = s.batch;
   base.m = m;
   base.n = n;
-  base.tm = tm;
-  base.tn = tn;
   base.status = reinterpret_cast<uint32_t*>(w + L.status);
   for (int step = 0; step < s.steps; ++step) {
     const int cur = step & 1;
     const bool last = step + 1 == s.steps;
     cudaError_t e;
+    NsMaps maps;
     // A = X X^T
     NsArgs g = base;
-    g.tiles = tm * (tm + 1) / 2;
     g.kblocks = (n + BK - 1) / BK;
     g.alpha = kScaleA / (kScaleX * kScaleX);
+    g.out_planes = TERMS == 3 ? 2 : 1;
     g.out_hi = ah;
     g.out_lo = al;
     g.out_ld = lda;
     g.out_bs = bsa;
-    e = launch_ns<MODE_GRAM, TERMS>(xk[cur][0], xk[cur][1], xk[cur][0], xk[cur][1], g, stream);
+    for (int p = 0; p < 2; ++p) {
+      maps.a[p] = x128[cur][p];
+      maps.b[p] = xb[cur][p];
+      maps.add[p] = a128[p];
+      maps.out[p] = a128[p];
+    }
+    e = launch_ns<MODE_GRAM, TERMS, CG, TN>(maps, g, stream);
     if (e != cudaSuccess) return e;
     // B = b A + c A A
     NsArgs p = g;
     p.kblocks = (m + BK - 1) / BK;
     p.alpha = s.c / kScaleA;
     p.beta = s.b;
-    p.add_hi = ah;
-    p.add_lo = al;
-    p.add_ld = lda;
-    p.add_bs = bsa;
+    p.add_planes = g.out_planes;
     p.out_hi = bh;
     p.out_lo = bl;
-    e = launch_ns<MODE_POLY, TERMS>(ma[0], ma[1], ma[0], ma[1], p, stream);
+    for (int q = 0; q < 2; ++q) {
+      maps.a[q] = a128[q];
+      maps.b[q] = ab[q];
+      maps.add[q] = a128[q];
+      maps.out[q] = b128[q];
+    }
+    e = launch_ns<MODE_POLY, TERMS, CG, TN>(maps, p, stream);
     if (e != cudaSuccess) return e;
-    // X = a X + B X
+    // X = a X + B X; the last step of one-term products adds X's high plane
+    // alone, so the step before it writes no other
     NsArgs x = base;
-    x.tiles = tm * tn;
     x.kblocks = (m + BK - 1) / BK;
     x.alpha = 1.f / kScaleA;
     x.beta = s.a;
-    x.add_hi = reinterpret_cast<__half*>(w + L.xh[cur]);
-    x.add_lo = TERMS == 3 || !last ? reinterpret_cast<__half*>(w + L.xl[cur]) : nullptr;
-    x.add_ld = ldx;
-    x.add_bs = bsx;
+    x.add_planes = TERMS == 3 || !last ? 2 : 1;
+    x.out_planes = TERMS == 3 || step + 2 < s.steps ? 2 : 1;
+    for (int q = 0; q < 2; ++q) {
+      maps.a[q] = b128[q];
+      maps.b[q] = xk[cur][q];
+      maps.add[q] = x128[cur][q];
+      maps.out[q] = x128[cur ^ 1][q];
+    }
     if (last) {
       x.alpha *= s.scale / kScaleX;
       x.beta *= s.scale / kScaleX;
@@ -787,15 +989,9 @@ cudaError_t run_steps(const OrthoShape& s, void* out, void* ws, cudaStream_t str
       x.out_trans = trans;
       x.o_ld = s.out_ld;
       x.o_bs = s.out_bs;
-      e = launch_ns<MODE_LAST, TERMS>(mb[0], mb[1], xn[cur][0], xn[cur][1], x, stream);
+      e = launch_ns<MODE_LAST, TERMS, CG, TN>(maps, x, stream);
     } else {
-      // the last step of bf16 results adds X's high plane alone
-      const bool lo = TERMS == 3 || step + 2 < s.steps;
-      x.out_hi = reinterpret_cast<__half*>(w + L.xh[cur ^ 1]);
-      x.out_lo = lo ? reinterpret_cast<__half*>(w + L.xl[cur ^ 1]) : nullptr;
-      x.out_ld = ldx;
-      x.out_bs = bsx;
-      e = launch_ns<MODE_APPLY, TERMS>(mb[0], mb[1], xn[cur][0], xn[cur][1], x, stream);
+      e = launch_ns<MODE_APPLY, TERMS, CG, TN>(maps, x, stream);
     }
     if (e != cudaSuccess) return e;
   }
@@ -835,7 +1031,12 @@ cudaError_t orthogonalize(const OrthoShape& s, const void* g, void* out, void* w
   cudaError_t e = s.in_bf16 ? run_init(s, static_cast<const __nv_bfloat16*>(g), ws, stream)
                             : run_init(s, static_cast<const float*>(g), ws, stream);
   if (e != cudaSuccess) return e;
-  return three_terms(s) ? run_steps<3>(s, out, ws, stream) : run_steps<1>(s, out, ws, stream);
+  const int m = s.rows < s.cols ? s.rows : s.cols, n = s.rows < s.cols ? s.cols : s.rows;
+  if (small_tiles(s.batch, m, n))
+    return three_terms(s) ? run_steps<3, 1, 64>(s, out, ws, stream)
+                          : run_steps<1, 1, 64>(s, out, ws, stream);
+  return three_terms(s) ? run_steps<3, 2, 256>(s, out, ws, stream)
+                        : run_steps<1, 2, 256>(s, out, ws, stream);
 }
 
 // The polynomial p(x) = a x + b x^3 + c x^5 keeps the fp16 planes in range
