@@ -80,8 +80,10 @@ struct Cfg {
   static constexpr int A_BYTES = 128 * BK * 2;              // one plane, one CTA
   static constexpr int B_BYTES = TN / CG * BK * 2;
   static constexpr int STAGE_BYTES = PLANES * (A_BYTES + B_BYTES);
-  static constexpr int EPI_BUFS = STAGE_BYTES >= 65536 ? 1 : 2;
-  static constexpr int EPI_BYTES = EPI_BUFS * 2 * PLANE_BYTES;
+  // chunk planes: 3 chunks of two planes where a tile has several chunks and
+  // the stages leave the room (96 KB of planes)
+  static constexpr int EPI_PLANES = STAGE_BYTES >= 65536 ? 2 : TN > 64 ? 6 : 4;
+  static constexpr int EPI_BYTES = EPI_PLANES * PLANE_BYTES;
   static constexpr int STAGES_MAX = (232448 - 1280 - EPI_BYTES) / STAGE_BYTES;
   static constexpr int STAGES = STAGES_MAX > 8 ? 8 : STAGES_MAX;
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_BYTES + 1024 + 256;
@@ -89,10 +91,25 @@ struct Cfg {
   static_assert(STAGES >= 2 && SMEM_BYTES <= 232448, "shared memory");
 };
 
+// Chunk buffers of a launch: planes of one, and how many there are.
+template <int MODE, int TERMS, int CG, int TN>
+struct Chunks {
+  static constexpr int OWN = TERMS == 3 || MODE == MODE_APPLY ? 2 : 1;
+  // gram, poly: as many again for the mirrored tile, where there is room
+  // (else it is stored from the registers)
+  static constexpr bool STAGED = (MODE == MODE_GRAM || MODE == MODE_POLY) &&
+                                 Cfg<TERMS, CG, TN>::EPI_PLANES >= 2 * OWN;
+  static constexpr int PLANES = STAGED ? 2 * OWN : OWN;
+  static constexpr int BUFS = Cfg<TERMS, CG, TN>::EPI_PLANES / PLANES;
+  static constexpr int BYTES = PLANES * PLANE_BYTES;
+};
+constexpr int MAX_BUFS = 6;
+
 struct NsArgs {
   int batch, m, n;
   int tm, tn;               // tiles of a matrix along its rows and columns
   int tiles;                // tiles of a matrix that are computed
+  int full;                 // gram, poly: all tiles are, none is mirrored
   int kblocks;              // BK-wide blocks of the inner dimension
   float alpha;              // factor of the accumulator
   float beta;               // factor of the added matrix (poly: A, apply: X)
@@ -142,6 +159,13 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
       : "memory");
 }
 
+// Wait until at most N of this thread's committed bulk stores still read
+// their shared memory.
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+
 template <int CG>
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                     uint32_t accumulate) {
@@ -155,16 +179,17 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
   if constexpr (CG == 2) tc_commit_pair(bar); else tc_commit(bar);
 }
 
-__device__ __forceinline__ uint32_t half2_bits(__half a, __half b) {
-  __half2 v = __halves2half2(a, b);
+__device__ __forceinline__ uint32_t half2_bits(__half2 v) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
 // Tile t of a matrix: rows i, columns j.  The symmetric products compute the
-// tiles that reach the diagonal or lie above it, j >= i TM / TN, row by row.
+// tiles that reach the diagonal or lie above it, j >= i TM / TN, row by row
+// (all tiles where every one has a CTA of its own: mirroring would only add
+// to the launch's last microseconds).
 template <int MODE, int RATIO>
 __device__ __forceinline__ void tile_of(const NsArgs& a, int t, int& i, int& j) {
-  if (MODE == MODE_GRAM || MODE == MODE_POLY) {
+  if ((MODE == MODE_GRAM || MODE == MODE_POLY) && !a.full) {
     i = 0;
     while (t >= a.tn - RATIO * i) {
       t -= a.tn - RATIO * i;
@@ -186,7 +211,7 @@ __device__ __forceinline__ uint4* piece(uint8_t* plane, int row, int c) {
 // of the matrix: the added planes' part, read from the chunk buffer, and the
 // result's planes, left in their place there.  `half`: which 32 columns of
 // the chunk.
-template <int MODE>
+template <int MODE, bool STAGED>
 __device__ __forceinline__ void finish32(const NsArgs& a, const float (&acc)[32], uint8_t* buf,
                                          int b, int row, int r, int c0, int half, bool mirror,
                                          int lane) {
@@ -290,11 +315,13 @@ __device__ __forceinline__ void finish32(const NsArgs& a, const float (&acc)[32]
     uint32_t w[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const __half h0 = __float2half_rn(v[2 * i]), h1 = __float2half_rn(v[2 * i + 1]);
-      w[i] = half2_bits(h0, h1);
+      // two at a time: the packed conversion runs at full rate
+      const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = half2_bits(h);
       if (p == 0) {   // what the high plane leaves
-        v[2 * i] -= __half2float(h0);
-        v[2 * i + 1] -= __half2float(h1);
+        const float2 f = __half22float2(h);
+        v[2 * i] -= f.x;
+        v[2 * i + 1] -= f.y;
       }
     }
 #pragma unroll
@@ -302,7 +329,22 @@ __device__ __forceinline__ void finish32(const NsArgs& a, const float (&acc)[32]
       *piece(buf + p * PLANE_BYTES, row, half * 4 + i) =
           make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     if (MODE == MODE_GRAM || MODE == MODE_POLY) {
-      if (mirror) {
+      if (STAGED && mirror) {
+        // the mirrored tile: 64 of its rows (this chunk's columns) in two
+        // boxes of 64 columns; two lanes exchange a column pair, so that each
+        // stores two neighbouring rows' values of one column
+        const int odd = lane & 1, rr = row & ~1;
+        uint8_t* box = buf + (a.out_planes + p) * PLANE_BYTES + (rr >> 6) * BOX_MN;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const uint32_t other = __shfl_xor_sync(0xffffffffu, w[i], 1);
+          const uint32_t st = odd ? __byte_perm(other, w[i], 0x7632)
+                                  : __byte_perm(w[i], other, 0x5410);
+          const int y = half * 32 + 2 * i + odd;
+          *reinterpret_cast<uint32_t*>(box + y * 128 + ((((rr & 63) >> 3) ^ (y & 7)) << 4) +
+                                       (rr & 7) * 2) = st;
+        }
+      } else if (mirror) {
         // the mirrored tile, straight to memory: two lanes exchange a column
         // pair, so that each stores two neighbouring rows' values of one column
         __half* plane = (p == 0 ? a.out_hi : a.out_lo) + static_cast<size_t>(b) * a.out_bs;
@@ -326,6 +368,7 @@ __device__ __forceinline__ void finish32(const NsArgs& a, const float (&acc)[32]
 // both in chunks of 128 rows x 64 columns.
 struct NsMaps {
   CUtensorMap a[2], b[2], add[2], out[2];
+  CUtensorMap mir[2];   // gram, poly: the result in boxes of 64 rows x 64 columns
 };
 
 template <int MODE, int TERMS, int CG, int TN>
@@ -336,6 +379,9 @@ ns_gemm_kernel(const __grid_constant__ NsMaps maps, const NsArgs args) {
   constexpr int RATIO = C::TM / TN;
   constexpr bool BMN = MODE == MODE_APPLY || MODE == MODE_LAST;
   constexpr uint32_t IDESC = idesc_f16_f32(C::TM, TN, BMN);
+  constexpr int BUFS = Chunks<MODE, TERMS, CG, TN>::BUFS;
+  constexpr int BUF_BYTES = Chunks<MODE, TERMS, CG, TN>::BYTES;
+  static_assert(BUFS >= 1 && BUFS <= MAX_BUFS, "chunk buffers");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -346,8 +392,8 @@ ns_gemm_kernel(const __grid_constant__ NsMaps maps, const NsArgs args) {
   uint64_t* tfull_bar = bars + 2 * STAGES;        // both copies
   uint64_t* tempty_bar = bars + 2 * STAGES + 2;   // rank 0's copy
   uint64_t* ready_bar = bars + 2 * STAGES + 4;    // a chunk buffer may be used
-  uint64_t* done_bar = bars + 2 * STAGES + 6;     // and has been
-  uint64_t* drain_bar = bars + 2 * STAGES + 8;
+  uint64_t* done_bar = ready_bar + MAX_BUFS;      // and has been
+  uint64_t* drain_bar = done_bar + MAX_BUFS;
   __shared__ uint32_t s_tmem_base;
   __shared__ int s_abort;
 
@@ -367,6 +413,8 @@ ns_gemm_kernel(const __grid_constant__ NsMaps maps, const NsArgs args) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull_bar[i], 1);
       mbar_init(&tempty_bar[i], CG * EPI_WARPS);
+    }
+    for (int i = 0; i < BUFS; ++i) {
       mbar_init(&ready_bar[i], 1);
       mbar_init(&done_bar[i], EPI_WARPS);
     }
@@ -505,7 +553,7 @@ ns_gemm_kernel(const __grid_constant__ NsMaps maps, const NsArgs args) {
         } else {
           mbar_arrive_expect_tx(&ready_bar[buf], args.add_planes * PLANE_BYTES);
           for (int p = 0; p < args.add_planes; ++p)
-            tma_load_3d<1>(sEpi + (buf * 2 + p) * PLANE_BYTES, &maps.add[p], &ready_bar[buf],
+            tma_load_3d<1>(sEpi + buf * BUF_BYTES + p * PLANE_BYTES, &maps.add[p], &ready_bar[buf],
                            tj * TN + in_c * 64, ti * C::TM + static_cast<int>(rank) * 128, b);
         }
         if (++in_c == TN / 64) {
@@ -513,7 +561,8 @@ ns_gemm_kernel(const __grid_constant__ NsMaps maps, const NsArgs args) {
           in_t += units;
         }
       };
-      for (int i = 0; i < C::EPI_BUFS; ++i) make_ready(i);
+      for (int i = 0; i < BUFS; ++i) make_ready(i);
+      int held = -1;   // the buffer whose store may still be reading it
       bool ok = true;
       int s = 0;
       for (long long t = unit; t < total && ok; t += units) {
@@ -523,25 +572,46 @@ ns_gemm_kernel(const __grid_constant__ NsMaps maps, const NsArgs args) {
                              ti, tj);
         const int ncols = BMN ? args.n : args.m;
         for (int c = 0; c < TN / 64; ++c, ++s) {
-          const int buf = s % C::EPI_BUFS;
-          if (!mbar_wait(&done_bar[buf], (s / C::EPI_BUFS) & 1, abort_flag)) { ok = false; break; }
+          const int buf = s % BUFS;
+          if (!mbar_wait(&done_bar[buf], (s / BUFS) & 1, abort_flag)) { ok = false; break; }
           const int row = ti * C::TM + static_cast<int>(rank) * 128, col = tj * TN + c * 64;
-          if (MODE != MODE_LAST && row < args.m && col < ncols) {
+          const bool store = MODE != MODE_LAST && row < args.m && col < ncols;
+          if (store) {
             for (int p = 0; p < args.out_planes; ++p)
-              tma_store_3d(&maps.out[p], sEpi + (buf * 2 + p) * PLANE_BYTES, col, row, b);
+              tma_store_3d(&maps.out[p], sEpi + buf * BUF_BYTES + p * PLANE_BYTES, col, row, b);
+            if (Chunks<MODE, TERMS, CG, TN>::STAGED && !args.full && tj >= RATIO * (ti + 1)) {
+              for (int p = 0; p < args.out_planes; ++p)
+                for (int x = 0; x < 128 && row + x < args.m; x += 64)
+                  tma_store_3d(&maps.mir[p],
+                               sEpi + buf * BUF_BYTES + (args.out_planes + p) * PLANE_BYTES +
+                                   (x / 64) * BOX_MN,
+                               row + x, col, b);
+            }
             bulk_commit();
-            bulk_wait_read_all();   // the buffer may be written again
           }
-          make_ready(buf);
+          // a buffer is handed on one chunk late, while its successor's store
+          // is in flight
+          if (held >= 0) {
+            if (store) bulk_wait_read<1>(); else bulk_wait_read<0>();
+            make_ready(held);
+            held = -1;
+          }
+          if (!store) {
+            make_ready(buf);
+          } else if (BUFS == 1) {
+            bulk_wait_read<0>();
+            make_ready(buf);
+          } else {
+            held = buf;
+          }
         }
       }
       bulk_wait_all();
       if (!ok && MODE != MODE_GRAM) {
         // let the chunk loads in flight land
-        for (int i = 0; i < C::EPI_BUFS; ++i) {
+        for (int i = 0; i < BUFS; ++i) {
           const unsigned long long t0 = globaltimer_ns();
-          const uint32_t par = ((s + ((i - s % C::EPI_BUFS) + C::EPI_BUFS) % C::EPI_BUFS) /
-                                C::EPI_BUFS) & 1;
+          const uint32_t par = ((s + ((i - s % BUFS) + BUFS) % BUFS) / BUFS) & 1;
           while (!mbar_try_wait(&ready_bar[i], par))
             if (globaltimer_ns() - t0 > kWaitLimitNs) break;
         }
@@ -571,12 +641,12 @@ ns_gemm_kernel(const __grid_constant__ NsMaps maps, const NsArgs args) {
       tile_of<MODE, RATIO>(args, static_cast<int>(t - static_cast<long long>(b) * args.tiles), ti,
                            tj);
       const int r = ti * C::TM + static_cast<int>(rank) * 128 + row;
-      const bool mirror = tj >= RATIO * (ti + 1);
+      const bool mirror = !args.full && tj >= RATIO * (ti + 1);
       // one chunk: its buffer, the 32 sums, and the hand-over to the mover
       auto chunk = [&](int c, const float (&f)[32]) {
-        const int buf = s % C::EPI_BUFS;
-        if (!wait(&ready_bar[buf], (s / C::EPI_BUFS) & 1)) return false;
-        finish32<MODE>(args, f, sEpi + buf * 2 * PLANE_BYTES, b, row, r, tj * TN + c * 64 + half * 32,
+        const int buf = s % BUFS;
+        if (!wait(&ready_bar[buf], (s / BUFS) & 1)) return false;
+        finish32<MODE, Chunks<MODE, TERMS, CG, TN>::STAGED>(args, f, sEpi + buf * BUF_BYTES, b, row, r, tj * TN + c * 64 + half * 32,
                        half, mirror, lane);
         fence_async_shared();
         __syncwarp();
@@ -649,8 +719,58 @@ ns_gemm_kernel(const __grid_constant__ NsMaps maps, const NsArgs args) {
   }
 }
 
-// ----------------------------------------------------- norm and first iterate
-constexpr int kSumThreads = 256;
+// ------------------------------------------- up to 128 rows: one launch in all
+// A matrix with m <= 128 (and n <= 2048) stays in the shared memory of one
+// cluster for the whole iteration: CTA `rank` of CL holds the columns
+// [64 nbx rank, 64 nbx (rank + 1)) of X, and every CTA all of A and B, as pairs of
+// planes in boxes of 128 rows x 64 columns (one layout serves as the
+// K-major operands of the gram and poly products and as the MN-major one of
+// the apply product).  Per step:
+//   gram    each CTA multiplies its columns (K = 64 nbx); the CL partial
+//           products meet in their rows' owners through distributed shared
+//           memory, are added there in rank order in fp32, and A's planes go
+//           to every CTA
+//   poly    B = b A + c A A, by every CTA for itself, in A's place
+//   apply   X = a X + B X on its own columns, in place
+// Three terms for both result types: with one tile a CTA the products cost
+// little.  What bounds it is latency: four block barriers and three cluster
+// barriers a step and their exchanges; 17 launches of the tiled kernel, 4 us
+// each with all their loads and stores, become one.
+constexpr int CL_ROWS = 128;
+constexpr int CL_BOX = CL_ROWS * 128;            // bytes of a box's plane
+constexpr int CL_MAX_BOXES = 4;                  // of X per CTA
+constexpr int CL_THREADS = 256;
+constexpr int CL_RECV_LD = 132;                  // floats of a received row
+constexpr int CL_RECV_BYTES = CL_ROWS * CL_RECV_LD * 4;
+
+struct ClArgs {
+  int batch, m, n, nbx, steps;
+  float a, b, c, scale;
+  double eps;
+  const void* g;
+  long long g_ld, g_bs;
+  void* out;
+  int out_bf16;
+  long long o_ld, o_bs;
+  int recv_apart;     // the receive buffer has its own place, else A's
+  uint32_t* status;
+};
+
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};"
+               ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void st_cluster_f64(uint32_t addr, double v) {
+  asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
+}
+__device__ __forceinline__ void fence_proxy_async_all() {
+  asm volatile("fence.proxy.async;" ::: "memory");
+}
 
 template <typename T>
 __device__ __forceinline__ float to_f32(T v);
@@ -660,6 +780,394 @@ template <>
 __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) {
   return __bfloat162float(v);
 }
+
+// Splits 8 values into 16-byte pieces of the two planes.
+__device__ __forceinline__ void split8(const float* v, uint4& hi, uint4& lo) {
+  uint32_t* wh = reinterpret_cast<uint32_t*>(&hi);
+  uint32_t* wl = reinterpret_cast<uint32_t*>(&lo);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+    const float2 f = __half22float2(h);
+    wh[i] = half2_bits(h);
+    wl[i] = half2_bits(__floats2half2_rn(v[2 * i] - f.x, v[2 * i + 1] - f.y));
+  }
+}
+
+// v = beta (hi + lo) + v over 8 elements of a row.
+__device__ __forceinline__ void add8(const uint4& hi, const uint4& lo, float beta, float* v) {
+  const __half2* h = reinterpret_cast<const __half2*>(&hi);
+  const __half2* l = reinterpret_cast<const __half2*>(&lo);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(h[i]), g = __half22float2(l[i]);
+    v[2 * i] = fmaf(beta, f.x + g.x, v[2 * i]);
+    v[2 * i + 1] = fmaf(beta, f.y + g.y, v[2 * i + 1]);
+  }
+}
+
+template <typename T, bool TRANS, int CL>
+__global__ void __launch_bounds__(CL_THREADS, 1)
+ns_cluster_kernel(const ClArgs args) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int nbx = args.nbx;
+  uint8_t* xh = smem;                              // X: nbx boxes of each plane
+  uint8_t* xl = xh + nbx * CL_BOX;
+  uint8_t* ah = xl + nbx * CL_BOX;                 // A, then B: two boxes of each
+  uint8_t* al = ah + 2 * CL_BOX;
+  float* recv = reinterpret_cast<float*>(args.recv_apart ? al + 2 * CL_BOX : ah);
+  __shared__ uint64_t s_bar;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  __shared__ double s_part[CL_THREADS / 32];
+  __shared__ double s_norm[8];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = CL > 1 ? cluster_ctarank() : 0u;
+  const int b = blockIdx.x / CL;
+  const int m = args.m;
+  const int c_first = 64 * nbx * static_cast<int>(rank);   // first column of this CTA
+  const T* g = static_cast<const T*>(args.g) + static_cast<size_t>(b) * args.g_bs;
+
+  pdl_trigger();
+  if (tid == 0) {
+    s_abort = 0;
+    mbar_init(&s_bar, 1);
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&s_tmem, 512);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  if (blockIdx.x == 0 && tid == 0) *args.status = 0u;   // the call's status starts clear
+  // ------------------------------------------------------------- the norm
+  double acc = 0.0;
+  const int c_end = min(c_first + 64 * nbx, args.n);
+  if (!TRANS) {
+    for (int r = warp; r < m; r += CL_THREADS / 32)
+#pragma unroll 4
+      for (int c = c_first + lane; c < c_end; c += 32) {
+        const double d = to_f32<T>(g[static_cast<size_t>(r) * args.g_ld + c]);
+        acc = fma(d, d, acc);
+      }
+  } else {
+    for (int c = c_first + warp; c < c_end; c += CL_THREADS / 32)
+#pragma unroll 4
+      for (int r = lane; r < m; r += 32) {
+        const double d = to_f32<T>(g[static_cast<size_t>(c) * args.g_ld + r]);
+        acc = fma(d, d, acc);
+      }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+  if (lane == 0) s_part[warp] = acc;
+  __syncthreads();
+  if (tid == 0) {
+    double t = 0.0;
+    for (int w = 0; w < CL_THREADS / 32; ++w) t += s_part[w];
+    if (CL == 1) s_norm[0] = t;
+    else
+      for (uint32_t q = 0; q < CL; ++q) st_cluster_f64(map_rank(smem_u32(&s_norm[rank]), q), t);
+  }
+  tc_fence_before();
+  if constexpr (CL > 1) cluster_sync_all(); else __syncthreads();
+  tc_fence_after();
+  double norm2 = 0.0;
+#pragma unroll
+  for (int q = 0; q < CL; ++q) norm2 += s_norm[q];
+  const float inv = static_cast<float>(static_cast<double>(kScaleX) / (sqrt(norm2) + args.eps));
+  const uint32_t tmem = s_tmem;
+  volatile int* abort_flag = &s_abort;
+  // --------------------------------------------------------- first iterate
+  if (!TRANS) {
+    // a warp per row, two columns per lane
+    for (int bx = 0; bx < nbx; ++bx)
+#pragma unroll 4
+      for (int r = warp; r < CL_ROWS; r += CL_THREADS / 32) {
+        const int c = c_first + 64 * bx + 2 * lane;
+        const T* p = g + static_cast<size_t>(r) * args.g_ld + c;
+        const float v0 = r < m && c < args.n ? to_f32<T>(p[0]) * inv : 0.f;
+        const float v1 = r < m && c + 1 < args.n ? to_f32<T>(p[1]) * inv : 0.f;
+        const __half2 h = __floats2half2_rn(v0, v1);
+        const float2 f = __half22float2(h);
+        const int off = bx * CL_BOX + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
+        *reinterpret_cast<uint32_t*>(xh + off) = half2_bits(h);
+        *reinterpret_cast<uint32_t*>(xl + off) =
+            half2_bits(__floats2half2_rn(v0 - f.x, v1 - f.y));
+      }
+  } else {
+    // a warp per column, lanes along the rows
+    for (int cc = warp; cc < 64 * nbx; cc += CL_THREADS / 32) {
+      const int c = c_first + cc;
+#pragma unroll
+      for (int r0 = 0; r0 < CL_ROWS; r0 += 32) {
+        const int r = r0 + lane;
+        const float v = r < m && c < args.n
+                            ? to_f32<T>(g[static_cast<size_t>(c) * args.g_ld + r]) * inv
+                            : 0.f;
+        const __half h = __float2half_rn(v);
+        const int off = (cc >> 6) * CL_BOX + r * 128 + ((((cc & 63) >> 3) ^ (r & 7)) << 4) +
+                        (cc & 7) * 2;
+        *reinterpret_cast<__half*>(xh + off) = h;
+        *reinterpret_cast<__half*>(xl + off) = __float2half_rn(v - __half2float(h));
+      }
+    }
+  }
+  // ----------------------------------------------------------------- steps
+  const int q = warp & 3, half = warp >> 2;        // rows, and half of the columns
+  const int row = q * 32 + lane;
+  const uint32_t lane_addr = static_cast<uint32_t>(q * 32) << 16;
+  const uint32_t d_sq = tmem, d_x = tmem + 128;    // accumulators: A or A A, B X
+  const int mp = (m + 15) & ~15;                   // rows that are not all zero
+  const uint32_t id_sq = idesc_f16_f32(128, mp, false);
+  const uint32_t id_x = idesc_f16_f32(128, 64 * nbx, true);
+  uint32_t phase = 0;
+  auto mma_done = [&]() {   // every thread waits for the issued products
+    mbar_wait(&s_bar, phase, abort_flag);
+    phase ^= 1u;
+    tc_fence_after();
+  };
+  for (int step = 0; step < args.steps; ++step) {
+    const bool last = step + 1 == args.steps;
+    fence_proxy_async_all();
+    tc_fence_before();
+    __syncthreads();
+    // ----------------------------------------------------------------- gram
+    if (tid == 0) {
+      tc_fence_after();
+      uint32_t first = 0;
+      for (int term = 0; term < 3; ++term)   // hi lo, lo hi, hi hi
+        for (int bx = 0; bx < nbx; ++bx) {
+          const uint32_t pa = smem_u32(term == 1 ? xl : xh) + bx * CL_BOX;
+          const uint32_t pb = smem_u32(term == 0 ? xl : xh) + bx * CL_BOX;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            tc_mma_f16(d_sq, smem_desc_sw128(pa + kk * 32), smem_desc_sw128(pb + kk * 32), id_sq,
+                       first);
+            first = 1u;
+          }
+        }
+      tc_commit(&s_bar);
+    }
+    mma_done();
+    const float alpha = kScaleA / (kScaleX * kScaleX);
+    if constexpr (CL == 1) {
+#pragma unroll
+      for (int c = 0; c < 64; c += 16) {
+        const int col = half * 64 + c;
+        if (col >= mp) break;                      // warp-uniform
+        uint32_t v[16];
+        tmem_ld16(d_sq + lane_addr + col, v);
+        tmem_ld_wait();
+        float f[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[i] = alpha * __uint_as_float(v[i]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint4 hi, lo;
+          split8(f + 8 * i, hi, lo);
+          *piece(ah + half * CL_BOX, row, (c >> 3) + i) = hi;
+          *piece(al + half * CL_BOX, row, (c >> 3) + i) = lo;
+        }
+      }
+    } else {
+      constexpr int R = CL_ROWS / CL;              // rows a CTA owns
+      // where rows are received in A's place, no CTA may still be multiplying
+      // by what the last step left there
+      if (!args.recv_apart) cluster_sync_all();
+      // partial rows to their owners: [source rank][row of the owner]
+      const uint32_t dst = map_rank(
+          smem_u32(recv + (static_cast<int>(rank) * R + row % R) * CL_RECV_LD + half * 64),
+          row / R);
+#pragma unroll
+      for (int c = 0; c < 64; c += 16) {
+        if (half * 64 + c >= mp) break;
+        uint32_t v[16];
+        tmem_ld16(d_sq + lane_addr + half * 64 + c, v);
+        tmem_ld_wait();
+        if (row < mp)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            st_cluster(dst + (c + 4 * i) * 4,
+                       make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+      }
+      tc_fence_before();
+      cluster_sync_all();
+      constexpr int PER = R * 16 / CL_THREADS > 0 ? R * 16 / CL_THREADS : 1;   // 8-column pieces
+      float f[PER][8];
+#pragma unroll
+      for (int u = 0; u < PER; ++u) {
+        const int item = u * CL_THREADS + tid, rr = item >> 4, cc = (item & 15) * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[u][i] = 0.f;
+        if (rr < R && static_cast<int>(rank) * R + rr < mp && cc < mp)
+          for (int s = 0; s < CL; ++s) {
+            const float4* p =
+                reinterpret_cast<const float4*>(recv + (s * R + rr) * CL_RECV_LD + cc);
+            const float4 x = p[0], y = p[1];
+            f[u][0] += x.x; f[u][1] += x.y; f[u][2] += x.z; f[u][3] += x.w;
+            f[u][4] += y.x; f[u][5] += y.y; f[u][6] += y.z; f[u][7] += y.w;
+          }
+      }
+      if (!args.recv_apart) cluster_sync_all();    // the sums are out of A's place
+#pragma unroll
+      for (int u = 0; u < PER; ++u) {
+        const int item = u * CL_THREADS + tid, rr = item >> 4, cc = (item & 15) * 8;
+        if (rr >= R) continue;
+        const int r = static_cast<int>(rank) * R + rr;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[u][i] *= alpha;
+        uint4 hi, lo;
+        split8(f[u], hi, lo);
+        const uint32_t ph = smem_u32(piece(ah + (cc >> 6) * CL_BOX, r, (cc & 63) >> 3));
+        const uint32_t pl = smem_u32(piece(al + (cc >> 6) * CL_BOX, r, (cc & 63) >> 3));
+#pragma unroll
+        for (uint32_t t = 0; t < CL; ++t) {
+          st_cluster(map_rank(ph, t), hi);
+          st_cluster(map_rank(pl, t), lo);
+        }
+      }
+      fence_proxy_async_all();
+      cluster_sync_all();
+    }
+    fence_proxy_async_all();
+    tc_fence_before();
+    __syncthreads();
+    // ----------------------------------------------------------------- poly
+    if (tid == 0) {
+      tc_fence_after();
+      uint32_t first = 0;
+      for (int term = 0; term < 3; ++term)
+        for (int k = 0; k < mp; k += 16) {
+          const uint32_t off = (k >> 6) * CL_BOX + (k & 63) * 2;
+          tc_mma_f16(d_sq, smem_desc_sw128(smem_u32(term == 1 ? al : ah) + off),
+                     smem_desc_sw128(smem_u32(term == 0 ? al : ah) + off), id_sq, first);
+          first = 1u;
+        }
+      tc_commit(&s_bar);
+    }
+    mma_done();
+#pragma unroll
+    for (int c = 0; c < 64; c += 16) {
+      const int col = half * 64 + c;
+      if (col >= mp) break;
+      uint32_t v[16];
+      tmem_ld16(d_sq + lane_addr + col, v);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = args.c / kScaleA * __uint_as_float(v[8 * i + e]);
+        uint4* ph = piece(ah + half * CL_BOX, row, (c >> 3) + i);
+        uint4* pl = piece(al + half * CL_BOX, row, (c >> 3) + i);
+        add8(*ph, *pl, args.b, f);
+        uint4 hi, lo;
+        split8(f, hi, lo);
+        *ph = hi;
+        *pl = lo;
+      }
+    }
+    fence_proxy_async_all();
+    tc_fence_before();
+    __syncthreads();
+    // ---------------------------------------------------------------- apply
+    if (tid == 0) {
+      tc_fence_after();
+      uint32_t first = 0;
+      for (int term = 0; term < 3; ++term)
+        for (int k = 0; k < mp; k += 16) {
+          const uint32_t off = (k >> 6) * CL_BOX + (k & 63) * 2;
+          tc_mma_f16(d_x, smem_desc_sw128(smem_u32(term == 1 ? al : ah) + off),
+                     smem_desc_sw128_mn(smem_u32(term == 0 ? xl : xh) + k * 128, CL_BOX), id_x,
+                     first);
+          first = 1u;
+        }
+      tc_commit(&s_bar);
+    }
+    mma_done();
+    const float xs = last ? args.scale / kScaleX : 1.f;
+    for (int bx = 0; bx < nbx; ++bx) {
+      float f[32];
+#pragma unroll
+      for (int c = 0; c < 32; c += 16) {
+        uint32_t v[16];
+        tmem_ld16(d_x + lane_addr + bx * 64 + half * 32 + c, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[c + i] = xs / kScaleA * __uint_as_float(v[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        add8(*piece(xh + bx * CL_BOX, row, half * 4 + i), *piece(xl + bx * CL_BOX, row, half * 4 + i),
+             xs * args.a, f + 8 * i);
+      if (!last) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint4 hi, lo;
+          split8(f + 8 * i, hi, lo);
+          *piece(xh + bx * CL_BOX, row, half * 4 + i) = hi;
+          *piece(xl + bx * CL_BOX, row, half * 4 + i) = lo;
+        }
+        continue;
+      }
+      const int c0 = c_first + bx * 64;            // of the box
+      if (TRANS) {
+        // X[r][c] is out[c][r]: neighbouring lanes store neighbouring elements
+        const size_t base = static_cast<size_t>(b) * args.o_bs + row;
+        if (row < m)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int c = c0 + half * 32 + i;
+            if (c >= args.n) continue;
+            const size_t o = base + static_cast<size_t>(c) * args.o_ld;
+            if (args.out_bf16)
+              static_cast<__nv_bfloat16*>(args.out)[o] = __float2bfloat16_rn(f[i]);
+            else
+              static_cast<float*>(args.out)[o] = f[i];
+          }
+      } else {
+        // through the box's planes (fp32: columns 0-31 in the first, 32-63 in
+        // the second), then along the rows
+        __syncthreads();
+        uint8_t* place = half == 0 ? xh + bx * CL_BOX : xl + bx * CL_BOX;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *piece(place, row, i) =
+              make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]),
+                         __float_as_uint(f[4 * i + 2]), __float_as_uint(f[4 * i + 3]));
+        __syncthreads();
+        for (int r = warp; r < m; r += CL_THREADS / 32)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int c = c0 + h * 32 + lane;
+            if (c >= args.n) continue;
+            const float v = reinterpret_cast<const float*>(
+                piece(h == 0 ? xh + bx * CL_BOX : xl + bx * CL_BOX, r, lane >> 2))[lane & 3];
+            const size_t o = static_cast<size_t>(b) * args.o_bs +
+                             static_cast<size_t>(r) * args.o_ld + c;
+            if (args.out_bf16)
+              static_cast<__nv_bfloat16*>(args.out)[o] = __float2bfloat16_rn(v);
+            else
+              static_cast<float*>(args.out)[o] = v;
+          }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && s_abort) atomicOr(args.status, kDevTimeout);
+  if (warp == 0) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ----------------------------------------------------- norm and first iterate
+constexpr int kSumThreads = 256;
 
 // Partial sums of squares in fp64 (squares of large or tiny gradients leave
 // fp32's range): block (chunk, matrix) takes every nchunk-th row.
@@ -755,10 +1263,10 @@ ortho_init_kernel(const T* __restrict__ g, long long ld, long long bs,
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float v0 = tile[y][x + 2 * e] * inv, v1 = tile[y][x + 2 * e + 1] * inv;
-      const __half h0 = __float2half_rn(v0), h1 = __float2half_rn(v1);
-      wh[e] = half2_bits(h0, h1);
-      wl[e] = half2_bits(__float2half_rn(v0 - __half2float(h0)),
-                         __float2half_rn(v1 - __half2float(h1)));
+      const __half2 h = __floats2half2_rn(v0, v1);
+      const float2 f = __half22float2(h);
+      wh[e] = half2_bits(h);
+      wl[e] = half2_bits(__floats2half2_rn(v0 - f.x, v1 - f.y));
     }
     const size_t at = static_cast<size_t>(b) * out_bs + static_cast<size_t>(r) * out_ld + c;
     *reinterpret_cast<uint4*>(hi + at) = qh;
@@ -826,13 +1334,14 @@ cudaError_t launch_ns(const NsMaps& maps, NsArgs args, cudaStream_t stream) {
   constexpr bool SYM = MODE == MODE_GRAM || MODE == MODE_POLY;
   args.tm = (args.m + C::TM - 1) / C::TM;
   args.tn = ((SYM ? args.m : args.n) + TN - 1) / TN;
+  const int max_units = num_sms() / CG;
   args.tiles = 0;
-  if (SYM)
+  args.full = SYM && static_cast<long long>(args.batch) * args.tm * args.tn <= max_units;
+  if (SYM && !args.full)
     for (int i = 0; i < args.tm; ++i) args.tiles += args.tn - C::TM / TN * i;
   else
     args.tiles = args.tm * args.tn;
   const long long total = static_cast<long long>(args.batch) * args.tiles;
-  const int max_units = num_sms() / CG;
   const int units = static_cast<int>(total < max_units ? total : max_units);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(CG * units);
@@ -895,6 +1404,89 @@ OrthoLayout ortho_layout(const OrthoShape& s) {
   return L;
 }
 
+// CTAs per cluster of the one-launch kernel, 0 where it does not apply.
+// Columns go to as many CTAs as keep two boxes each while every matrix has
+// its cluster at once; else four boxes each.
+int cluster_size(int batch, int m, int n) {
+  if (m > CL_ROWS || n > 8 * CL_MAX_BOXES * 64) return 0;
+  const int boxes = (n + 63) / 64;
+  int wide = 1, narrow = 1;   // by four and by two boxes a CTA
+  while (wide * CL_MAX_BOXES < boxes) wide *= 2;
+  while (narrow * 2 < boxes && narrow < 8) narrow *= 2;
+  return static_cast<long long>(batch) * narrow <= 128 ? narrow : wide;
+}
+
+template <typename T, bool TRANS, int CL>
+cudaError_t launch_cluster(const ClArgs& args, int smem, cudaStream_t stream) {
+  auto kern = ns_cluster_kernel<T, TRANS, CL>;
+  static std::atomic<unsigned long long> attr_done{0};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (!(attr_done.load(std::memory_order_acquire) & bit)) {
+    cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448 - 256);
+    if (e != cudaSuccess) return e;
+    attr_done.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(CL * args.batch);
+  cfg.blockDim = dim3(CL_THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CL;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, args);
+}
+
+template <typename T>
+cudaError_t run_cluster(const OrthoShape& s, int cl, const void* g, void* out, void* ws,
+                        cudaStream_t stream) {
+  const bool trans = s.rows > s.cols;
+  ClArgs a{};
+  a.batch = s.batch;
+  a.m = trans ? s.cols : s.rows;
+  a.n = trans ? s.rows : s.cols;
+  a.nbx = ((a.n + 63) / 64 + cl - 1) / cl;
+  a.steps = s.steps;
+  a.a = s.a;
+  a.b = s.b;
+  a.c = s.c;
+  a.scale = s.scale;
+  a.eps = static_cast<double>(s.eps);
+  a.g = g;
+  a.g_ld = s.g_ld;
+  a.g_bs = s.g_bs;
+  a.out = out;
+  a.out_bf16 = s.out_bf16;
+  a.o_ld = s.out_ld;
+  a.o_bs = s.out_bs;
+  a.status = static_cast<uint32_t*>(ws);
+  // X's and A's planes; the received rows apart while that fits, else in A's
+  // place (they are a little larger)
+  int smem = (2 * a.nbx + 4) * CL_BOX + 1024;
+  if (cl > 1) {
+    a.recv_apart = smem + CL_RECV_BYTES <= 232448 - 256;
+    smem += a.recv_apart ? CL_RECV_BYTES : CL_RECV_BYTES - 4 * CL_BOX;
+  }
+  auto go = [&](auto one, auto two, auto four, auto eight) {
+    return cl == 1 ? one(a, smem, stream)
+                   : cl == 2 ? two(a, smem, stream)
+                             : cl == 4 ? four(a, smem, stream) : eight(a, smem, stream);
+  };
+  return trans ? go(launch_cluster<T, true, 1>, launch_cluster<T, true, 2>,
+                    launch_cluster<T, true, 4>, launch_cluster<T, true, 8>)
+               : go(launch_cluster<T, false, 1>, launch_cluster<T, false, 2>,
+                    launch_cluster<T, false, 4>, launch_cluster<T, false, 8>);
+}
+
 // The steps with tiles of 128 CG x TN.
 template <int TERMS, int CG, int TN>
 cudaError_t run_steps(const OrthoShape& s, void* out, void* ws, cudaStream_t stream) {
@@ -909,8 +1501,9 @@ cudaError_t run_steps(const OrthoShape& s, void* out, void* ws, cudaStream_t str
   __half* bh = reinterpret_cast<__half*>(w + L.bh);
   __half* bl = TERMS == 3 ? reinterpret_cast<__half*>(w + L.bl) : nullptr;
   // maps by box rows: 128 (A operand, chunks), TN / CG (B operand, K-major),
-  // BK (X as the B operand of the apply product, MN-major)
-  CUtensorMap x128[2][2], xb[2][2], xk[2][2], a128[2], ab[2], b128[2];   // [buffer][plane]
+  // BK (X as the B operand of the apply product, MN-major), 64 (mirrored tiles)
+  CUtensorMap x128[2][2], xb[2][2], xk[2][2];   // [buffer][plane]
+  CUtensorMap a128[2], ab[2], a64[2], b128[2], b64[2];
   for (int i = 0; i < 2; ++i)
     for (int p = 0; p < 2; ++p) {
       const void* base = w + (p ? L.xl[i] : L.xh[i]);
@@ -922,7 +1515,9 @@ cudaError_t run_steps(const OrthoShape& s, void* out, void* ws, cudaStream_t str
   for (int p = 0; p < 2; ++p)
     if (!make_map3(&a128[p], p && al ? al : ah, m, m, lda, s.batch, bsa, 128) ||
         !make_map3(&ab[p], p && al ? al : ah, m, m, lda, s.batch, bsa, TN / CG) ||
-        !make_map3(&b128[p], p && bl ? bl : bh, m, m, lda, s.batch, bsa, 128))
+        !make_map3(&a64[p], p && al ? al : ah, m, m, lda, s.batch, bsa, 64) ||
+        !make_map3(&b128[p], p && bl ? bl : bh, m, m, lda, s.batch, bsa, 128) ||
+        !make_map3(&b64[p], p && bl ? bl : bh, m, m, lda, s.batch, bsa, 64))
       return cudaErrorInvalidValue;
   NsArgs base{};
   base.batch = s.batch;
@@ -948,6 +1543,7 @@ cudaError_t run_steps(const OrthoShape& s, void* out, void* ws, cudaStream_t str
       maps.b[p] = xb[cur][p];
       maps.add[p] = a128[p];
       maps.out[p] = a128[p];
+      maps.mir[p] = a64[p];
     }
     e = launch_ns<MODE_GRAM, TERMS, CG, TN>(maps, g, stream);
     if (e != cudaSuccess) return e;
@@ -964,6 +1560,7 @@ cudaError_t run_steps(const OrthoShape& s, void* out, void* ws, cudaStream_t str
       maps.b[q] = ab[q];
       maps.add[q] = a128[q];
       maps.out[q] = b128[q];
+      maps.mir[q] = b64[q];
     }
     e = launch_ns<MODE_POLY, TERMS, CG, TN>(maps, p, stream);
     if (e != cudaSuccess) return e;
@@ -1024,14 +1621,21 @@ cudaError_t run_init(const OrthoShape& s, const T* g, void* ws, cudaStream_t str
 
 }  // namespace
 
-size_t ortho_workspace(const OrthoShape& s) { return ortho_layout(s).total; }
+size_t ortho_workspace(const OrthoShape& s) {
+  const int m = s.rows < s.cols ? s.rows : s.cols, n = s.rows < s.cols ? s.cols : s.rows;
+  return cluster_size(s.batch, m, n) > 0 ? 256 : ortho_layout(s).total;   // 256: the status
+}
 
 cudaError_t orthogonalize(const OrthoShape& s, const void* g, void* out, void* ws,
                           cudaStream_t stream) {
+  const int m = s.rows < s.cols ? s.rows : s.cols, n = s.rows < s.cols ? s.cols : s.rows;
+  const int cl = cluster_size(s.batch, m, n);
+  if (cl > 0)
+    return s.in_bf16 ? run_cluster<__nv_bfloat16>(s, cl, g, out, ws, stream)
+                     : run_cluster<float>(s, cl, g, out, ws, stream);
   cudaError_t e = s.in_bf16 ? run_init(s, static_cast<const __nv_bfloat16*>(g), ws, stream)
                             : run_init(s, static_cast<const float*>(g), ws, stream);
   if (e != cudaSuccess) return e;
-  const int m = s.rows < s.cols ? s.rows : s.cols, n = s.rows < s.cols ? s.cols : s.rows;
   if (small_tiles(s.batch, m, n))
     return three_terms(s) ? run_steps<3, 1, 64>(s, out, ws, stream)
                           : run_steps<1, 1, 64>(s, out, ws, stream);
