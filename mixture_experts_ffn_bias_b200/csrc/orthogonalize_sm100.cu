@@ -739,9 +739,8 @@ ns_gemm_kernel(const __grid_constant__ NsMaps maps, const NsArgs args) {
 constexpr int CL_ROWS = 128;
 constexpr int CL_BOX = CL_ROWS * 128;            // bytes of a box's plane
 constexpr int CL_MAX_BOXES = 4;                  // of X per CTA
-constexpr int CL_THREADS = 256;
-constexpr int CL_RECV_LD = 132;                  // floats of a received row
-constexpr int CL_RECV_BYTES = CL_ROWS * CL_RECV_LD * 4;
+constexpr int CL_THREADS = 512;
+constexpr int CL_RECV_BYTES = CL_ROWS * CL_ROWS * 4;
 
 struct ClArgs {
   int batch, m, n, nbx, steps;
@@ -764,6 +763,9 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void st_cluster(uint32_t addr, const uint4& v) {
   asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};"
                ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 __device__ __forceinline__ void st_cluster_f64(uint32_t addr, double v) {
   asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
@@ -843,22 +845,39 @@ ns_cluster_kernel(const ClArgs args) {
   pdl_wait();
   if (blockIdx.x == 0 && tid == 0) *args.status = 0u;   // the call's status starts clear
   // ------------------------------------------------------------- the norm
+  // G is read once; until the norm is known its fp32 bits wait in the planes,
+  // the upper half in the first, the lower in the second.
   double acc = 0.0;
-  const int c_end = min(c_first + 64 * nbx, args.n);
   if (!TRANS) {
-    for (int r = warp; r < m; r += CL_THREADS / 32)
-#pragma unroll 4
-      for (int c = c_first + lane; c < c_end; c += 32) {
-        const double d = to_f32<T>(g[static_cast<size_t>(r) * args.g_ld + c]);
-        acc = fma(d, d, acc);
-      }
+    // a warp per row of a box, two columns per lane
+#pragma unroll 8
+    for (int i = warp; i < nbx * CL_ROWS; i += CL_THREADS / 32) {
+      const int bx = i / CL_ROWS, r = i % CL_ROWS;
+      const int c = c_first + 64 * bx + 2 * lane;
+      const T* p = g + static_cast<size_t>(r) * args.g_ld + c;
+      const float v0 = r < m && c < args.n ? to_f32<T>(p[0]) : 0.f;
+      const float v1 = r < m && c + 1 < args.n ? to_f32<T>(p[1]) : 0.f;
+      acc = fma(static_cast<double>(v0), static_cast<double>(v0), acc);
+      acc = fma(static_cast<double>(v1), static_cast<double>(v1), acc);
+      const int off = bx * CL_BOX + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
+      const uint32_t b0 = __float_as_uint(v0), b1 = __float_as_uint(v1);
+      *reinterpret_cast<uint32_t*>(xh + off) = __byte_perm(b0, b1, 0x7632);
+      *reinterpret_cast<uint32_t*>(xl + off) = __byte_perm(b0, b1, 0x5410);
+    }
   } else {
-    for (int c = c_first + warp; c < c_end; c += CL_THREADS / 32)
-#pragma unroll 4
-      for (int r = lane; r < m; r += 32) {
-        const double d = to_f32<T>(g[static_cast<size_t>(c) * args.g_ld + r]);
-        acc = fma(d, d, acc);
-      }
+    // a warp per 32 rows of a column
+#pragma unroll 8
+    for (int i = warp; i < 64 * nbx * 4; i += CL_THREADS / 32) {
+      const int cc = i >> 2, r = (i & 3) * 32 + lane, c = c_first + cc;
+      const float v = r < m && c < args.n
+                          ? to_f32<T>(g[static_cast<size_t>(c) * args.g_ld + r])
+                          : 0.f;
+      acc = fma(static_cast<double>(v), static_cast<double>(v), acc);
+      const int off = (cc >> 6) * CL_BOX + r * 128 + ((((cc & 63) >> 3) ^ (r & 7)) << 4) +
+                      (cc & 7) * 2;
+      *reinterpret_cast<uint16_t*>(xh + off) = static_cast<uint16_t>(__float_as_uint(v) >> 16);
+      *reinterpret_cast<uint16_t*>(xl + off) = static_cast<uint16_t>(__float_as_uint(v));
+    }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
@@ -881,49 +900,45 @@ ns_cluster_kernel(const ClArgs args) {
   const uint32_t tmem = s_tmem;
   volatile int* abort_flag = &s_abort;
   // --------------------------------------------------------- first iterate
-  if (!TRANS) {
-    // a warp per row, two columns per lane
-    for (int bx = 0; bx < nbx; ++bx)
-#pragma unroll 4
-      for (int r = warp; r < CL_ROWS; r += CL_THREADS / 32) {
-        const int c = c_first + 64 * bx + 2 * lane;
-        const T* p = g + static_cast<size_t>(r) * args.g_ld + c;
-        const float v0 = r < m && c < args.n ? to_f32<T>(p[0]) * inv : 0.f;
-        const float v1 = r < m && c + 1 < args.n ? to_f32<T>(p[1]) * inv : 0.f;
-        const __half2 h = __floats2half2_rn(v0, v1);
-        const float2 f = __half22float2(h);
-        const int off = bx * CL_BOX + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
-        *reinterpret_cast<uint32_t*>(xh + off) = half2_bits(h);
-        *reinterpret_cast<uint32_t*>(xl + off) =
-            half2_bits(__floats2half2_rn(v0 - f.x, v1 - f.y));
-      }
-  } else {
-    // a warp per column, lanes along the rows
-    for (int cc = warp; cc < 64 * nbx; cc += CL_THREADS / 32) {
-      const int c = c_first + cc;
+  // (the barrier above is the block's too)
+  for (int i = tid; i < nbx * CL_BOX / 16; i += CL_THREADS) {
+    uint4* ph = reinterpret_cast<uint4*>(xh) + i;
+    uint4* pl = reinterpret_cast<uint4*>(xl) + i;
+    const uint4 vh = *ph, vl = *pl;
+    const uint32_t* wh = reinterpret_cast<const uint32_t*>(&vh);
+    const uint32_t* wl = reinterpret_cast<const uint32_t*>(&vl);
+    float f[8];
 #pragma unroll
-      for (int r0 = 0; r0 < CL_ROWS; r0 += 32) {
-        const int r = r0 + lane;
-        const float v = r < m && c < args.n
-                            ? to_f32<T>(g[static_cast<size_t>(c) * args.g_ld + r]) * inv
-                            : 0.f;
-        const __half h = __float2half_rn(v);
-        const int off = (cc >> 6) * CL_BOX + r * 128 + ((((cc & 63) >> 3) ^ (r & 7)) << 4) +
-                        (cc & 7) * 2;
-        *reinterpret_cast<__half*>(xh + off) = h;
-        *reinterpret_cast<__half*>(xl + off) = __float2half_rn(v - __half2float(h));
-      }
+    for (int e = 0; e < 4; ++e) {
+      f[2 * e] = __uint_as_float(__byte_perm(wl[e], wh[e], 0x5410)) * inv;
+      f[2 * e + 1] = __uint_as_float(__byte_perm(wl[e], wh[e], 0x7632)) * inv;
     }
+    uint4 hi, lo;
+    split8(f, hi, lo);
+    *ph = hi;
+    *pl = lo;
   }
   // ----------------------------------------------------------------- steps
-  const int q = warp & 3, half = warp >> 2;        // rows, and half of the columns
+  const int q = warp & 3, quarter = warp >> 2;     // rows, and 32 of 128 columns
   const int row = q * 32 + lane;
+  const int sq_col = quarter * 32;                 // of A and B
+  uint8_t* sq_h = ah + (quarter >> 1) * CL_BOX;    // their box, and the piece in it
+  uint8_t* sq_l = al + (quarter >> 1) * CL_BOX;
+  const int sq_piece = (quarter & 1) * 4;
   const uint32_t lane_addr = static_cast<uint32_t>(q * 32) << 16;
   const uint32_t d_sq = tmem, d_x = tmem + 128;    // accumulators: A or A A, B X
   const int mp = (m + 15) & ~15;                   // rows that are not all zero
   const uint32_t id_sq = idesc_f16_f32(128, mp, false);
   const uint32_t id_x = idesc_f16_f32(128, 64 * nbx, true);
   uint32_t phase = 0;
+  auto load32 = [&](uint32_t taddr, float factor, float (&f)[32]) {
+    uint32_t v[32];
+    tmem_ld16(taddr + lane_addr, *reinterpret_cast<uint32_t(*)[16]>(&v[0]));
+    tmem_ld16(taddr + lane_addr + 16, *reinterpret_cast<uint32_t(*)[16]>(&v[16]));
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) f[i] = factor * __uint_as_float(v[i]);
+  };
   auto mma_done = [&]() {   // every thread waits for the issued products
     mbar_wait(&s_bar, phase, abort_flag);
     phase ^= 1u;
@@ -954,22 +969,15 @@ ns_cluster_kernel(const ClArgs args) {
     mma_done();
     const float alpha = kScaleA / (kScaleX * kScaleX);
     if constexpr (CL == 1) {
+      if (sq_col < mp) {                           // warp-uniform
+        float f[32];
+        load32(d_sq + sq_col, alpha, f);
 #pragma unroll
-      for (int c = 0; c < 64; c += 16) {
-        const int col = half * 64 + c;
-        if (col >= mp) break;                      // warp-uniform
-        uint32_t v[16];
-        tmem_ld16(d_sq + lane_addr + col, v);
-        tmem_ld_wait();
-        float f[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) f[i] = alpha * __uint_as_float(v[i]);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
           uint4 hi, lo;
           split8(f + 8 * i, hi, lo);
-          *piece(ah + half * CL_BOX, row, (c >> 3) + i) = hi;
-          *piece(al + half * CL_BOX, row, (c >> 3) + i) = lo;
+          *piece(sq_h, row, sq_piece + i) = hi;
+          *piece(sq_l, row, sq_piece + i) = lo;
         }
       }
     } else {
@@ -977,25 +985,23 @@ ns_cluster_kernel(const ClArgs args) {
       // where rows are received in A's place, no CTA may still be multiplying
       // by what the last step left there
       if (!args.recv_apart) cluster_sync_all();
-      // partial rows to their owners: [source rank][row of the owner]
-      const uint32_t dst = map_rank(
-          smem_u32(recv + (static_cast<int>(rank) * R + row % R) * CL_RECV_LD + half * 64),
-          row / R);
+      // Partial rows to their owners: [source rank][row of the owner][128].
+      // The partial product is symmetric, so a lane's 32 values of row r are
+      // sent as column r of 32 rows: a warp stores 32 neighbours at a time.
+      if (sq_col < mp && q * 32 < mp) {
+        float f[32];
+        load32(d_sq + sq_col, 1.f, f);
+        const uint32_t mine =
+            smem_u32(recv + static_cast<int>(rank) * R * CL_ROWS + row);
 #pragma unroll
-      for (int c = 0; c < 64; c += 16) {
-        if (half * 64 + c >= mp) break;
-        uint32_t v[16];
-        tmem_ld16(d_sq + lane_addr + half * 64 + c, v);
-        tmem_ld_wait();
-        if (row < mp)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            st_cluster(dst + (c + 4 * i) * 4,
-                       make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+        for (int i = 0; i < 32; ++i) {
+          const int c = sq_col + i;
+          st_cluster_f32(map_rank(mine + (c % R) * CL_ROWS * 4, c / R), f[i]);
+        }
       }
       tc_fence_before();
       cluster_sync_all();
-      constexpr int PER = R * 16 / CL_THREADS > 0 ? R * 16 / CL_THREADS : 1;   // 8-column pieces
+      constexpr int PER = (R * 16 + CL_THREADS - 1) / CL_THREADS;   // 8-column pieces
       float f[PER][8];
 #pragma unroll
       for (int u = 0; u < PER; ++u) {
@@ -1003,9 +1009,10 @@ ns_cluster_kernel(const ClArgs args) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[u][i] = 0.f;
         if (rr < R && static_cast<int>(rank) * R + rr < mp && cc < mp)
+#pragma unroll
           for (int s = 0; s < CL; ++s) {
             const float4* p =
-                reinterpret_cast<const float4*>(recv + (s * R + rr) * CL_RECV_LD + cc);
+                reinterpret_cast<const float4*>(recv + (s * R + rr) * CL_ROWS + cc);
             const float4 x = p[0], y = p[1];
             f[u][0] += x.x; f[u][1] += x.y; f[u][2] += x.z; f[u][3] += x.w;
             f[u][4] += y.x; f[u][5] += y.y; f[u][6] += y.z; f[u][7] += y.w;
@@ -1015,8 +1022,9 @@ ns_cluster_kernel(const ClArgs args) {
 #pragma unroll
       for (int u = 0; u < PER; ++u) {
         const int item = u * CL_THREADS + tid, rr = item >> 4, cc = (item & 15) * 8;
-        if (rr >= R) continue;
         const int r = static_cast<int>(rank) * R + rr;
+        // the rows and columns the products read
+        if (rr >= R || (cc >= mp && r >= mp)) continue;
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[u][i] *= alpha;
         uint4 hi, lo;
@@ -1024,7 +1032,8 @@ ns_cluster_kernel(const ClArgs args) {
         const uint32_t ph = smem_u32(piece(ah + (cc >> 6) * CL_BOX, r, (cc & 63) >> 3));
         const uint32_t pl = smem_u32(piece(al + (cc >> 6) * CL_BOX, r, (cc & 63) >> 3));
 #pragma unroll
-        for (uint32_t t = 0; t < CL; ++t) {
+        for (uint32_t i = 0; i < CL; ++i) {
+          const uint32_t t = (rank + i) % CL;      // not all to one CTA at a time
           st_cluster(map_rank(ph, t), hi);
           st_cluster(map_rank(pl, t), lo);
         }
@@ -1049,23 +1058,16 @@ ns_cluster_kernel(const ClArgs args) {
       tc_commit(&s_bar);
     }
     mma_done();
+    if (sq_col < mp) {
+      float f[32];
+      load32(d_sq + sq_col, args.c / kScaleA, f);
 #pragma unroll
-    for (int c = 0; c < 64; c += 16) {
-      const int col = half * 64 + c;
-      if (col >= mp) break;
-      uint32_t v[16];
-      tmem_ld16(d_sq + lane_addr + col, v);
-      tmem_ld_wait();
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float f[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = args.c / kScaleA * __uint_as_float(v[8 * i + e]);
-        uint4* ph = piece(ah + half * CL_BOX, row, (c >> 3) + i);
-        uint4* pl = piece(al + half * CL_BOX, row, (c >> 3) + i);
-        add8(*ph, *pl, args.b, f);
+      for (int i = 0; i < 4; ++i) {
+        uint4* ph = piece(sq_h, row, sq_piece + i);
+        uint4* pl = piece(sq_l, row, sq_piece + i);
+        add8(*ph, *pl, args.b, f + 8 * i);
         uint4 hi, lo;
-        split8(f, hi, lo);
+        split8(f + 8 * i, hi, lo);
         *ph = hi;
         *pl = lo;
       }
@@ -1089,35 +1091,33 @@ ns_cluster_kernel(const ClArgs args) {
     }
     mma_done();
     const float xs = last ? args.scale / kScaleX : 1.f;
-    for (int bx = 0; bx < nbx; ++bx) {
+    const int half = quarter & 1;                  // of a box's columns
+    // the warp's boxes: every other one
+    for (int b0 = 0; b0 < nbx; b0 += 2) {
+      const int bx = b0 + (quarter >> 1);
+      const bool have = bx < nbx;
       float f[32];
-#pragma unroll
-      for (int c = 0; c < 32; c += 16) {
-        uint32_t v[16];
-        tmem_ld16(d_x + lane_addr + bx * 64 + half * 32 + c, v);
-        tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 16; ++i) f[c + i] = xs / kScaleA * __uint_as_float(v[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        add8(*piece(xh + bx * CL_BOX, row, half * 4 + i), *piece(xl + bx * CL_BOX, row, half * 4 + i),
-             xs * args.a, f + 8 * i);
-      if (!last) {
+      if (have) {
+        load32(d_x + bx * 64 + half * 32, xs / kScaleA, f);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          uint4 hi, lo;
-          split8(f + 8 * i, hi, lo);
-          *piece(xh + bx * CL_BOX, row, half * 4 + i) = hi;
-          *piece(xl + bx * CL_BOX, row, half * 4 + i) = lo;
+          uint4* ph = piece(xh + bx * CL_BOX, row, half * 4 + i);
+          uint4* pl = piece(xl + bx * CL_BOX, row, half * 4 + i);
+          add8(*ph, *pl, xs * args.a, f + 8 * i);
+          if (!last) {
+            uint4 hi, lo;
+            split8(f + 8 * i, hi, lo);
+            *ph = hi;
+            *pl = lo;
+          }
         }
-        continue;
       }
+      if (!last) continue;
       const int c0 = c_first + bx * 64;            // of the box
       if (TRANS) {
         // X[r][c] is out[c][r]: neighbouring lanes store neighbouring elements
         const size_t base = static_cast<size_t>(b) * args.o_bs + row;
-        if (row < m)
+        if (have && row < m)
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const int c = c0 + half * 32 + i;
@@ -1132,20 +1132,25 @@ ns_cluster_kernel(const ClArgs args) {
         // through the box's planes (fp32: columns 0-31 in the first, 32-63 in
         // the second), then along the rows
         __syncthreads();
-        uint8_t* place = half == 0 ? xh + bx * CL_BOX : xl + bx * CL_BOX;
+        if (have) {
+          uint8_t* place = half == 0 ? xh + bx * CL_BOX : xl + bx * CL_BOX;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          *piece(place, row, i) =
-              make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]),
-                         __float_as_uint(f[4 * i + 2]), __float_as_uint(f[4 * i + 3]));
+          for (int i = 0; i < 8; ++i)
+            *piece(place, row, i) =
+                make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]),
+                           __float_as_uint(f[4 * i + 2]), __float_as_uint(f[4 * i + 3]));
+        }
         __syncthreads();
-        for (int r = warp; r < m; r += CL_THREADS / 32)
+#pragma unroll 4
+        for (int i = warp; i < 2 * CL_ROWS; i += CL_THREADS / 32) {
+          const int by = b0 + i / CL_ROWS, r = i % CL_ROWS;
+          if (by >= nbx || r >= m) continue;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int c = c0 + h * 32 + lane;
+            const int c = c_first + by * 64 + h * 32 + lane;
             if (c >= args.n) continue;
             const float v = reinterpret_cast<const float*>(
-                piece(h == 0 ? xh + bx * CL_BOX : xl + bx * CL_BOX, r, lane >> 2))[lane & 3];
+                piece(h == 0 ? xh + by * CL_BOX : xl + by * CL_BOX, r, lane >> 2))[lane & 3];
             const size_t o = static_cast<size_t>(b) * args.o_bs +
                              static_cast<size_t>(r) * args.o_ld + c;
             if (args.out_bf16)
@@ -1153,6 +1158,7 @@ ns_cluster_kernel(const ClArgs args) {
             else
               static_cast<float*>(args.out)[o] = v;
           }
+        }
       }
     }
   }
@@ -1425,7 +1431,7 @@ cudaError_t launch_cluster(const ClArgs& args, int smem, cudaStream_t stream) {
   const unsigned long long bit = 1ull << (dev & 63);
   if (!(attr_done.load(std::memory_order_acquire) & bit)) {
     cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448 - 256);
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448 - 512);
     if (e != cudaSuccess) return e;
     attr_done.fetch_or(bit, std::memory_order_acq_rel);
   }
@@ -1470,11 +1476,12 @@ cudaError_t run_cluster(const OrthoShape& s, int cl, const void* g, void* out, v
   a.o_bs = s.out_bs;
   a.status = static_cast<uint32_t*>(ws);
   // X's and A's planes; the received rows apart while that fits, else in A's
-  // place (they are a little larger)
+  // place (of the same size)
+  static_assert(CL_RECV_BYTES == 4 * CL_BOX, "A's planes");
   int smem = (2 * a.nbx + 4) * CL_BOX + 1024;
   if (cl > 1) {
-    a.recv_apart = smem + CL_RECV_BYTES <= 232448 - 256;
-    smem += a.recv_apart ? CL_RECV_BYTES : CL_RECV_BYTES - 4 * CL_BOX;
+    a.recv_apart = smem + CL_RECV_BYTES <= 232448 - 512;
+    if (a.recv_apart) smem += CL_RECV_BYTES;
   }
   auto go = [&](auto one, auto two, auto four, auto eight) {
     return cl == 1 ? one(a, smem, stream)
