@@ -82,7 +82,8 @@ struct Cfg {
   static constexpr int STAGE_BYTES = PLANES * (A_BYTES + B_BYTES);
   // chunk planes: 3 chunks of two planes where a tile has several chunks and
   // the stages leave the room (96 KB of planes)
-  static constexpr int EPI_PLANES = STAGE_BYTES >= 65536 ? 2 : TN > 64 ? 6 : 4;
+  static constexpr int EPI_PLANES =
+      STAGE_BYTES >= 65536 ? 2 : (STAGE_BYTES >= 49152 || TN == 64) ? 4 : 6;
   static constexpr int EPI_BYTES = EPI_PLANES * PLANE_BYTES;
   static constexpr int STAGES_MAX = (232448 - 1280 - EPI_BYTES) / STAGE_BYTES;
   static constexpr int STAGES = STAGES_MAX > 8 ? 8 : STAGES_MAX;
@@ -1374,12 +1375,6 @@ bool three_terms(const OrthoShape& s) {
   return !s.out_bf16 || (s.rows < s.cols ? s.rows : s.cols) < 64;
 }
 
-// Tiles of 128 x 64 on single CTAs instead of 256 x 256 on pairs.
-bool small_tiles(int batch, int m, int n) {
-  const long long big = static_cast<long long>(batch) * ((m + 255) / 256) * ((n + 255) / 256);
-  return big < 74;
-}
-
 struct OrthoLayout {
   size_t status, partial, xh[2], xl[2], ah, al, bh, bl, total;
 };
@@ -1494,8 +1489,55 @@ cudaError_t run_cluster(const OrthoShape& s, int cl, const void* g, void* out, v
                     launch_cluster<T, false, 4>, launch_cluster<T, false, 8>);
 }
 
-// The steps with tiles of 128 CG x TN.
-template <int TERMS, int CG, int TN>
+// Tile shapes of the tiled kernel: 256 x 256 and 256 x 128 on CTA pairs, 128 x 64
+// on single CTAs.
+enum TileShape { TILE_256, TILE_128, TILE_64 };
+
+// The shape with the least estimated time for one launch: rounds of tiles
+// over the SMs times k-blocks.  The cycles of a k-block are measured with all SMs
+// busy: staging an SM's operands from L2 (38 bytes a cycle) bounds them, so
+// the large tile moves the least per product, and the smaller ones win where
+// they fill the last round better.  epi: a tile's epilogue, hidden behind
+// the next tile's products but for the last.
+template <int MODE, int TERMS>
+TileShape choose_tiles(int batch, int m, int n, int kblocks) {
+  constexpr bool SYM = MODE == MODE_GRAM || MODE == MODE_POLY;
+  const struct { int tm, tn, units, kb, epi; } shapes[3] = {
+      {256, 256, num_sms() / 2, TERMS == 3 ? 1750 : 860, TERMS == 3 ? 6000 : 3500},
+      {256, 128, num_sms() / 2, TERMS == 3 ? 1260 : 650, TERMS == 3 ? 3500 : 2200},
+      {128, 64, num_sms(), TERMS == 3 ? 1050 : 560, TERMS == 3 ? 2200 : 1500}};
+  TileShape best = TILE_256;
+  long long least = -1;
+  for (int i = 0; i < 3; ++i) {
+    const auto& t = shapes[i];
+    const int tm = (m + t.tm - 1) / t.tm, tn = ((SYM ? m : n) + t.tn - 1) / t.tn;
+    long long tiles = static_cast<long long>(tm) * tn;
+    if (SYM && tiles * batch > t.units) {
+      tiles = 0;
+      for (int r = 0; r < tm; ++r) tiles += tn - t.tm / t.tn * r;
+    }
+    const long long rounds = (tiles * batch + t.units - 1) / t.units;
+    const long long work = static_cast<long long>(kblocks) * t.kb;
+    const long long cost = (rounds - 1) * (work > t.epi ? work : t.epi) + work + t.epi;
+    if (least < 0 || cost < least) {
+      least = cost;
+      best = static_cast<TileShape>(i);
+    }
+  }
+  return best;
+}
+
+template <int MODE, int TERMS>
+cudaError_t launch_best(NsMaps& maps, const CUtensorMap (&b_op)[3][2], const NsArgs& args,
+                        cudaStream_t stream) {
+  const TileShape t = choose_tiles<MODE, TERMS>(args.batch, args.m, args.n, args.kblocks);
+  for (int p = 0; p < 2; ++p) maps.b[p] = b_op[t][p];
+  return t == TILE_256   ? launch_ns<MODE, TERMS, 2, 256>(maps, args, stream)
+         : t == TILE_128 ? launch_ns<MODE, TERMS, 2, 128>(maps, args, stream)
+                         : launch_ns<MODE, TERMS, 1, 64>(maps, args, stream);
+}
+
+template <int TERMS>
 cudaError_t run_steps(const OrthoShape& s, void* out, void* ws, cudaStream_t stream) {
   const OrthoLayout L = ortho_layout(s);
   uint8_t* w = static_cast<uint8_t*>(ws);
@@ -1507,25 +1549,25 @@ cudaError_t run_steps(const OrthoShape& s, void* out, void* ws, cudaStream_t str
   __half* al = TERMS == 3 ? reinterpret_cast<__half*>(w + L.al) : nullptr;
   __half* bh = reinterpret_cast<__half*>(w + L.bh);
   __half* bl = TERMS == 3 ? reinterpret_cast<__half*>(w + L.bl) : nullptr;
-  // maps by box rows: 128 (A operand, chunks), TN / CG (B operand, K-major),
-  // BK (X as the B operand of the apply product, MN-major), 64 (mirrored tiles)
-  CUtensorMap x128[2][2], xb[2][2], xk[2][2];   // [buffer][plane]
-  CUtensorMap a128[2], ab[2], a64[2], b128[2], b64[2];
+  // Maps by box rows: 128 (A operand, chunks), 64 (mirrored tiles; X as the B
+  // operand of the apply product, MN-major).  The K-major B operand takes
+  // 128 rows a CTA of the 256 x 256 tile, 64 of the others.
+  CUtensorMap x128[2][2], x64[2][2];               // [buffer][plane]
+  CUtensorMap a128[2], a64[2], b128[2], b64[2];
   for (int i = 0; i < 2; ++i)
     for (int p = 0; p < 2; ++p) {
       const void* base = w + (p ? L.xl[i] : L.xh[i]);
       if (!make_map3(&x128[i][p], base, m, n, ldx, s.batch, bsx, 128) ||
-          !make_map3(&xb[i][p], base, m, n, ldx, s.batch, bsx, TN / CG) ||
-          !make_map3(&xk[i][p], base, m, n, ldx, s.batch, bsx, BK))
+          !make_map3(&x64[i][p], base, m, n, ldx, s.batch, bsx, 64))
         return cudaErrorInvalidValue;
     }
   for (int p = 0; p < 2; ++p)
     if (!make_map3(&a128[p], p && al ? al : ah, m, m, lda, s.batch, bsa, 128) ||
-        !make_map3(&ab[p], p && al ? al : ah, m, m, lda, s.batch, bsa, TN / CG) ||
         !make_map3(&a64[p], p && al ? al : ah, m, m, lda, s.batch, bsa, 64) ||
         !make_map3(&b128[p], p && bl ? bl : bh, m, m, lda, s.batch, bsa, 128) ||
         !make_map3(&b64[p], p && bl ? bl : bh, m, m, lda, s.batch, bsa, 64))
       return cudaErrorInvalidValue;
+  static_assert(BK == 64, "boxes of X in the apply product");
   NsArgs base{};
   base.batch = s.batch;
   base.m = m;
@@ -1545,14 +1587,16 @@ cudaError_t run_steps(const OrthoShape& s, void* out, void* ws, cudaStream_t str
     g.out_lo = al;
     g.out_ld = lda;
     g.out_bs = bsa;
+    CUtensorMap b_op[3][2];
     for (int p = 0; p < 2; ++p) {
       maps.a[p] = x128[cur][p];
-      maps.b[p] = xb[cur][p];
+      b_op[TILE_256][p] = x128[cur][p];
+      b_op[TILE_128][p] = b_op[TILE_64][p] = x64[cur][p];
       maps.add[p] = a128[p];
       maps.out[p] = a128[p];
       maps.mir[p] = a64[p];
     }
-    e = launch_ns<MODE_GRAM, TERMS, CG, TN>(maps, g, stream);
+    e = launch_best<MODE_GRAM, TERMS>(maps, b_op, g, stream);
     if (e != cudaSuccess) return e;
     // B = b A + c A A
     NsArgs p = g;
@@ -1564,12 +1608,13 @@ cudaError_t run_steps(const OrthoShape& s, void* out, void* ws, cudaStream_t str
     p.out_lo = bl;
     for (int q = 0; q < 2; ++q) {
       maps.a[q] = a128[q];
-      maps.b[q] = ab[q];
+      b_op[TILE_256][q] = a128[q];
+      b_op[TILE_128][q] = b_op[TILE_64][q] = a64[q];
       maps.add[q] = a128[q];
       maps.out[q] = b128[q];
       maps.mir[q] = b64[q];
     }
-    e = launch_ns<MODE_POLY, TERMS, CG, TN>(maps, p, stream);
+    e = launch_best<MODE_POLY, TERMS>(maps, b_op, p, stream);
     if (e != cudaSuccess) return e;
     // X = a X + B X; the last step of one-term products adds X's high plane
     // alone, so the step before it writes no other
@@ -1581,7 +1626,7 @@ cudaError_t run_steps(const OrthoShape& s, void* out, void* ws, cudaStream_t str
     x.out_planes = TERMS == 3 || step + 2 < s.steps ? 2 : 1;
     for (int q = 0; q < 2; ++q) {
       maps.a[q] = b128[q];
-      maps.b[q] = xk[cur][q];
+      for (int t = 0; t < 3; ++t) b_op[t][q] = x64[cur][q];
       maps.add[q] = x128[cur][q];
       maps.out[q] = x128[cur ^ 1][q];
     }
@@ -1593,9 +1638,9 @@ cudaError_t run_steps(const OrthoShape& s, void* out, void* ws, cudaStream_t str
       x.out_trans = trans;
       x.o_ld = s.out_ld;
       x.o_bs = s.out_bs;
-      e = launch_ns<MODE_LAST, TERMS, CG, TN>(maps, x, stream);
+      e = launch_best<MODE_LAST, TERMS>(maps, b_op, x, stream);
     } else {
-      e = launch_ns<MODE_APPLY, TERMS, CG, TN>(maps, x, stream);
+      e = launch_best<MODE_APPLY, TERMS>(maps, b_op, x, stream);
     }
     if (e != cudaSuccess) return e;
   }
@@ -1643,11 +1688,7 @@ cudaError_t orthogonalize(const OrthoShape& s, const void* g, void* out, void* w
   cudaError_t e = s.in_bf16 ? run_init(s, static_cast<const __nv_bfloat16*>(g), ws, stream)
                             : run_init(s, static_cast<const float*>(g), ws, stream);
   if (e != cudaSuccess) return e;
-  if (small_tiles(s.batch, m, n))
-    return three_terms(s) ? run_steps<3, 1, 64>(s, out, ws, stream)
-                          : run_steps<1, 1, 64>(s, out, ws, stream);
-  return three_terms(s) ? run_steps<3, 2, 256>(s, out, ws, stream)
-                        : run_steps<1, 2, 256>(s, out, ws, stream);
+  return three_terms(s) ? run_steps<3>(s, out, ws, stream) : run_steps<1>(s, out, ws, stream);
 }
 
 // The polynomial p(x) = a x + b x^3 + c x^5 keeps the fp16 planes in range
