@@ -1224,19 +1224,10 @@ ortho_sumsq_kernel(const T* __restrict__ g, int rows, int cols, long long ld, lo
   }
 }
 
-// X0 = G / (|G|_F + eps), scaled, as two fp16 planes [m, n]; TRANS: of G^T.
-// One block per 64 x 64 tile of X0.
-template <typename T, bool TRANS>
-__global__ void __launch_bounds__(256)
-ortho_init_kernel(const T* __restrict__ g, long long ld, long long bs,
-                  const double* __restrict__ partial, int nchunk, double eps, int m, int n,
-                  __half* __restrict__ hi, __half* __restrict__ lo, long long out_ld,
-                  long long out_bs) {
-  pdl_trigger();
-  pdl_wait();
+// kScaleX / (|G|_F + eps) of matrix b from its partial sums, to the block.
+__device__ __forceinline__ float scale_of(const double* __restrict__ partial, int nchunk, int b,
+                                          double eps) {
   __shared__ float s_inv;
-  __shared__ float tile[64][65];
-  const int b = blockIdx.z;
   if (threadIdx.x < 32) {
     double t = 0.0;
     for (int i = threadIdx.x; i < nchunk; i += 32) t += partial[static_cast<size_t>(b) * nchunk + i];
@@ -1245,39 +1236,109 @@ ortho_init_kernel(const T* __restrict__ g, long long ld, long long bs,
     if (threadIdx.x == 0)
       s_inv = static_cast<float>(static_cast<double>(kScaleX) / (sqrt(t) + eps));
   }
+  __syncthreads();
+  return s_inv;
+}
+
+// X0 = G / (|G|_F + eps), scaled, as two fp16 planes [m, n] with rows of ld_o
+// elements: pieces of 8 along the rows, four in flight a thread.
+template <typename T>
+__global__ void __launch_bounds__(256)
+ortho_scale_kernel(const T* __restrict__ g, long long ld, long long bs,
+                   const double* __restrict__ partial, int nchunk, double eps, int m, int n,
+                   __half* __restrict__ hi, __half* __restrict__ lo, int ld_o) {
+  pdl_trigger();
+  pdl_wait();
+  const int b = blockIdx.y;
+  const float inv = scale_of(partial, nchunk, b, eps);
+  const T* base = g + static_cast<size_t>(b) * bs;
+  const size_t obase = static_cast<size_t>(b) * m * ld_o;
+  constexpr int V = 16 / sizeof(T);
+  const bool vec = ld % V == 0 && (reinterpret_cast<uintptr_t>(base) & 15) == 0;
+  const int per_row = ld_o / 8;
+  const long long pieces = static_cast<long long>(m) * per_row;
+  constexpr int U = 4;
+  for (long long p0 = blockIdx.x * 256ll * U; p0 < pieces; p0 += gridDim.x * 256ll * U) {
+    float v[U][8];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long long p = p0 + u * 256 + threadIdx.x;
+      const int r = static_cast<int>(p / per_row), c = static_cast<int>(p % per_row) * 8;
+      const T* src = base + static_cast<size_t>(r) * ld + c;
+      if (p < pieces && vec && c + 8 <= n) {
+#pragma unroll
+        for (int h = 0; h < 8 / V; ++h) {
+          const uint4 q = __ldcs(reinterpret_cast<const uint4*>(src) + h);
+          const T* e = reinterpret_cast<const T*>(&q);
+#pragma unroll
+          for (int k = 0; k < V; ++k) v[u][h * V + k] = to_f32<T>(e[k]);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[u][k] = p < pieces && c + k < n ? to_f32<T>(src[k]) : 0.f;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long long p = p0 + u * 256 + threadIdx.x;
+      if (p >= pieces) continue;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[u][k] *= inv;
+      uint4 h, l;
+      split8(v[u], h, l);
+      *reinterpret_cast<uint4*>(hi + obase + p * 8) = h;
+      *reinterpret_cast<uint4*>(lo + obase + p * 8) = l;
+    }
+  }
+}
+
+// The same of G^T, by tiles of 64 x 64.
+template <typename T>
+__global__ void __launch_bounds__(256)
+ortho_transpose_kernel(const T* __restrict__ g, long long ld, long long bs,
+                       const double* __restrict__ partial, int nchunk, double eps, int m, int n,
+                       __half* __restrict__ hi, __half* __restrict__ lo, int ld_o) {
+  pdl_trigger();
+  pdl_wait();
+  __shared__ float tile[64][65];
+  const int b = blockIdx.z;
   const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;   // of X0
   const T* base = g + static_cast<size_t>(b) * bs;
-  // 64 x 64 elements, 16 per thread, along G's rows
+  constexpr int V = 16 / sizeof(T);
+  if (ld % V == 0 && (reinterpret_cast<uintptr_t>(base) & 15) == 0 && r0 + 64 <= m) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int y = (threadIdx.x >> 6) + 4 * i, x = threadIdx.x & 63;
-    const int gr = (TRANS ? c0 : r0) + y, gc = (TRANS ? r0 : c0) + x;
-    const int rows = TRANS ? n : m, cols = TRANS ? m : n;
-    const float v = gr < rows && gc < cols ? to_f32<T>(base[static_cast<size_t>(gr) * ld + gc])
-                                           : 0.f;
-    if (TRANS) tile[x][y] = v; else tile[y][x] = v;
+    for (int i = 0; i < 64 * 64 / V / 256; ++i) {
+      const int item = i * 256 + threadIdx.x, y = item / (64 / V), x = item % (64 / V) * V;
+      uint4 q = make_uint4(0u, 0u, 0u, 0u);
+      if (c0 + y < n)
+        q = __ldcs(reinterpret_cast<const uint4*>(base + static_cast<size_t>(c0 + y) * ld + r0 + x));
+      const T* e = reinterpret_cast<const T*>(&q);
+#pragma unroll
+      for (int k = 0; k < V; ++k) tile[x + k][y] = to_f32<T>(e[k]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int y = (threadIdx.x >> 6) + 4 * i, x = threadIdx.x & 63;
+      tile[x][y] = c0 + y < n && r0 + x < m
+                       ? to_f32<T>(base[static_cast<size_t>(c0 + y) * ld + r0 + x])
+                       : 0.f;
+    }
   }
-  __syncthreads();
-  const float inv = s_inv;
+  const float inv = scale_of(partial, nchunk, b, eps);   // and the tile is complete
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int y = (threadIdx.x >> 3) + 32 * i, x = (threadIdx.x & 7) * 8;
     const int r = r0 + y, c = c0 + x;
-    if (r >= m || c >= out_ld) continue;
-    uint4 qh, ql;
-    uint32_t* wh = reinterpret_cast<uint32_t*>(&qh);
-    uint32_t* wl = reinterpret_cast<uint32_t*>(&ql);
+    if (r >= m || c >= ld_o) continue;
+    float v[8];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float v0 = tile[y][x + 2 * e] * inv, v1 = tile[y][x + 2 * e + 1] * inv;
-      const __half2 h = __floats2half2_rn(v0, v1);
-      const float2 f = __half22float2(h);
-      wh[e] = half2_bits(h);
-      wl[e] = half2_bits(__floats2half2_rn(v0 - f.x, v1 - f.y));
-    }
-    const size_t at = static_cast<size_t>(b) * out_bs + static_cast<size_t>(r) * out_ld + c;
-    *reinterpret_cast<uint4*>(hi + at) = qh;
-    *reinterpret_cast<uint4*>(lo + at) = ql;
+    for (int e = 0; e < 8; ++e) v[e] = tile[y][x + e] * inv;
+    uint4 h, l;
+    split8(v, h, l);
+    const size_t at = (static_cast<size_t>(b) * m + r) * ld_o + c;
+    *reinterpret_cast<uint4*>(hi + at) = h;
+    *reinterpret_cast<uint4*>(lo + at) = l;
   }
 }
 
@@ -1379,9 +1440,10 @@ struct OrthoLayout {
   size_t status, partial, xh[2], xl[2], ah, al, bh, bl, total;
 };
 
-int sum_chunks(int rows) {
+int sum_chunks(int rows, int batch) {
   const int c = (rows + 8 - 1) / 8;   // eight rows (one per warp) at least
-  return c < 64 ? c : 64;
+  const int most = 2048 / batch > 32 ? 2048 / batch : 32;
+  return c < most ? c : most;
 }
 
 OrthoLayout ortho_layout(const OrthoShape& s) {
@@ -1392,7 +1454,7 @@ OrthoLayout ortho_layout(const OrthoShape& s) {
   OrthoLayout L{};
   size_t o = 0;
   L.status = o;  o += 256;
-  L.partial = o; o += up256(static_cast<size_t>(s.batch) * sum_chunks(s.rows) * 8);
+  L.partial = o; o += up256(static_cast<size_t>(s.batch) * sum_chunks(s.rows, s.batch) * 8);
   for (int i = 0; i < 2; ++i) {
     L.xh[i] = o; o += up256(x);
     L.xl[i] = o; o += up256(x);
@@ -1498,14 +1560,19 @@ enum TileShape { TILE_256, TILE_128, TILE_64 };
 // busy: staging an SM's operands from L2 (38 bytes a cycle) bounds them, so
 // the large tile moves the least per product, and the smaller ones win where
 // they fill the last round better.  epi: a tile's epilogue, hidden behind
-// the next tile's products but for the last.
+// the next tile's products but for the last; it is what a short inner
+// dimension leaves visible, and long where chunks wait for their buffer (the
+// large tile's stages of four planes leave room for one).
 template <int MODE, int TERMS>
 TileShape choose_tiles(int batch, int m, int n, int kblocks) {
   constexpr bool SYM = MODE == MODE_GRAM || MODE == MODE_POLY;
   const struct { int tm, tn, units, kb, epi; } shapes[3] = {
-      {256, 256, num_sms() / 2, TERMS == 3 ? 1750 : 860, TERMS == 3 ? 6000 : 3500},
-      {256, 128, num_sms() / 2, TERMS == 3 ? 1260 : 650, TERMS == 3 ? 3500 : 2200},
-      {128, 64, num_sms(), TERMS == 3 ? 1050 : 560, TERMS == 3 ? 2200 : 1500}};
+      {256, 256, num_sms() / 2, TERMS == 3 ? 1750 : 860,
+       TERMS == 3 ? (SYM ? 20000 : 16000) : SYM ? 4500 : 7500},
+      {256, 128, num_sms() / 2, TERMS == 3 ? 1260 : 650,
+       TERMS == 3 ? (SYM ? 4500 : 6000) : SYM ? 2500 : 4200},
+      {128, 64, num_sms(), TERMS == 3 ? 1050 : 560,
+       TERMS == 3 ? (SYM ? 2500 : 2800) : SYM ? 1500 : 2000}};
   TileShape best = TILE_256;
   long long least = -1;
   for (int i = 0; i < 3; ++i) {
@@ -1653,22 +1720,28 @@ cudaError_t run_init(const OrthoShape& s, const T* g, void* ws, cudaStream_t str
   uint8_t* w = static_cast<uint8_t*>(ws);
   const bool trans = s.rows > s.cols;
   const int m = trans ? s.cols : s.rows, n = trans ? s.rows : s.cols;
-  const int nchunk = sum_chunks(s.rows);
+  const int nchunk = sum_chunks(s.rows, s.batch);
   double* partial = reinterpret_cast<double*>(w + L.partial);
   cudaError_t e =
       launch_pdl(ortho_sumsq_kernel<T>, dim3(nchunk, s.batch), dim3(kSumThreads), 0, stream, g,
                  s.rows, s.cols, s.g_ld, s.g_bs, partial,
                  reinterpret_cast<uint32_t*>(w + L.status));
   if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>(pad64(n) / 64), static_cast<unsigned>(pad64(m) / 64),
-                  s.batch);
   __half* hi = reinterpret_cast<__half*>(w + L.xh[0]);
   __half* lo = reinterpret_cast<__half*>(w + L.xl[0]);
-  const long long ldx = pad64(n);
-  return launch_pdl(trans ? ortho_init_kernel<T, true> : ortho_init_kernel<T, false>, grid,
-                    dim3(256), 0, stream, g, s.g_ld, s.g_bs,
-                    static_cast<const double*>(partial), nchunk, static_cast<double>(s.eps), m, n,
-                    hi, lo, ldx, ldx * m);
+  const int ldx = static_cast<int>(pad64(n));
+  const double* sums = partial;
+  const double eps = static_cast<double>(s.eps);
+  if (trans)
+    return launch_pdl(ortho_transpose_kernel<T>,
+                      dim3(static_cast<unsigned>(ldx / 64), static_cast<unsigned>(pad64(m) / 64),
+                           s.batch),
+                      dim3(256), 0, stream, g, s.g_ld, s.g_bs, sums, nchunk, eps, m, n, hi, lo, ldx);
+  const long long blocks = (static_cast<long long>(m) * (ldx / 8) + 1023) / 1024;
+  const int most = num_sms() * 16 / s.batch > 8 ? num_sms() * 16 / s.batch : 8;
+  return launch_pdl(ortho_scale_kernel<T>,
+                    dim3(static_cast<unsigned>(blocks < most ? blocks : most), s.batch), dim3(256),
+                    0, stream, g, s.g_ld, s.g_bs, sums, nchunk, eps, m, n, hi, lo, ldx);
 }
 
 }  // namespace
