@@ -568,3 +568,31 @@ def test_dispatch_reports_missing_experts_outside_the_layer_call():
                   torch.empty(4, 2, **i32), torch.empty(8, **i32),
                   torch.empty(8, 128, dtype=torch.bfloat16, device="cuda"), ws)
     assert B.moe_device_status(ws)[0] == B.MOE_ERR_DATA
+
+
+def test_binding_refuses_tensors_it_cannot_pass_on():
+    """Other types, too small, not dense, or on the host: refused before a launch."""
+    l = _logits(8, 16, 1)
+    cfg, o = B.make_config(8, 128, 16, 128, 2), B.make_group_opts(4, 2)
+    idx = torch.full((8, 2), -7, dtype=torch.int32, device="cuda")
+    w = torch.full((8, 2), -7.0, device="cuda")
+    dl = torch.full((8, 16), -7.0, device="cuda")
+    bias, mask = torch.zeros(16, device="cuda"), torch.ones(8, device="cuda")
+    bad = [(l.double(), None, None, idx, w), (l.cpu(), None, None, idx, w),
+           (l, None, None, idx.long(), w), (l, None, None, idx.cpu(), w),
+           (l, None, None, idx[:4], w), (l, None, None, idx, w.t()),
+           (l, bias[:8], None, idx, w), (l, bias.double(), None, idx, w), (l, None, mask, idx, w)]
+    for args in bad:
+        with pytest.raises(B.MoEError):
+            B.moe_route_groups(cfg, o, *args)
+    for args in [(l, idx.long(), w, dl), (l, idx, w.cpu(), dl), (l, idx, w, dl.half()),
+                 (l, idx, w[:1], dl), (l.cpu(), idx, w, dl)]:
+        with pytest.raises(B.MoEError):
+            B.moe_route_groups_backward(cfg, o, *args)
+    oc = B.make_ortho_config(1, 8, 16, B.DTYPE_F32, B.DTYPE_F32)
+    ws = torch.empty(4096, dtype=torch.uint8, device="cuda")
+    for g, out in [(l.half(), dl), (l, dl.half()), (l.cpu(), dl), (l, dl.cpu())]:
+        with pytest.raises(B.MoEError):
+            B.moe_orthogonalize(oc, g, out, ws)
+    torch.cuda.synchronize()
+    assert torch.all(idx == -7) and torch.all(w == -7.0) and torch.all(dl == -7.0)
