@@ -1378,11 +1378,19 @@ bool make_map3(CUtensorMap* map, const void* base, int rows, int cols, long long
          CUDA_SUCCESS;
 }
 
+// SMs of the current device, asked for once per device.
 int num_sms() {
-  int dev = 0, n = 0;
+  static std::atomic<int> known[64];
+  int dev = 0;
   cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n > 0 ? n : 148;
+  std::atomic<int>& k = known[dev & 63];
+  int n = k.load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (n <= 0) n = 148;
+    k.store(n, std::memory_order_relaxed);
+  }
+  return n;
 }
 
 template <int MODE, int TERMS, int CG, int TN>
@@ -1566,12 +1574,13 @@ enum TileShape { TILE_256, TILE_128, TILE_64 };
 template <int MODE, int TERMS>
 TileShape choose_tiles(int batch, int m, int n, int kblocks) {
   constexpr bool SYM = MODE == MODE_GRAM || MODE == MODE_POLY;
+  const int sms = num_sms();
   const struct { int tm, tn, units, kb, epi; } shapes[3] = {
-      {256, 256, num_sms() / 2, TERMS == 3 ? 1750 : 860,
+      {256, 256, sms / 2, TERMS == 3 ? 1750 : 860,
        TERMS == 3 ? (SYM ? 20000 : 16000) : SYM ? 4500 : 7500},
-      {256, 128, num_sms() / 2, TERMS == 3 ? 1260 : 650,
+      {256, 128, sms / 2, TERMS == 3 ? 1260 : 650,
        TERMS == 3 ? (SYM ? 4500 : 6000) : SYM ? 2500 : 4200},
-      {128, 64, num_sms(), TERMS == 3 ? 1050 : 560,
+      {128, 64, sms, TERMS == 3 ? 1050 : 560,
        TERMS == 3 ? (SYM ? 2500 : 2800) : SYM ? 1500 : 2000}};
   TileShape best = TILE_256;
   long long least = -1;
