@@ -49,10 +49,15 @@ __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) {
 
 // Shared-memory position of expert e: 4 floats of padding per 32, so that
 // the 8 lanes of a token, a group or E/8 experts apart, read 16-byte pieces
-// from different banks.  And the expert at a position (below 36 * 8): p / 36
-// as a multiplication.
+// from different banks.
 __device__ __forceinline__ int at(int e) { return e + ((e >> 5) << 2); }
-__device__ __forceinline__ int expert_at(int p) { return p - 4 * ((p * 1821) >> 16); }
+// The expert of a pick: positions are below 36 * 8, and p / 36 is taken by way
+// of a multiplication; a pick's position is its block's place and, from bit 16, the
+// expert in the block.
+__device__ __forceinline__ int expert_at(int x) {
+  const int p = (x & 0xffff) + (x >> 16);
+  return p - 4 * ((p * 1821) >> 16);
+}
 
 // A key above -inf as an integer in the keys' order, never 0.
 __device__ __forceinline__ unsigned long long ordered(double v) {
@@ -84,11 +89,12 @@ __device__ __noinline__ void order_picks_f64(const RouteShape& a, const L* __res
                                              int2* picks) {
   double m = 0.0, sum = 1.0;
   if (a.gate == 0 && a.space == 1) softmax_f64(a, row, lane, m, sum);
-  int2 p = make_int2(1 << 30, 0);
+  int2 p = make_int2(0, 0);
   double key = -INFINITY;
+  int e = kMaxE;
   if (lane < count) {
     p = picks[lane];
-    const int e = expert_at(p.x);
+    e = expert_at(p.x);
     key = to_f64(row[e]);
     if (a.space == 1) key = a.gate == 0 ? exp(key - m) / sum : 1.0 / (1.0 + exp(-key));
     if (bias != nullptr) key += static_cast<double>(bias[e]);
@@ -96,8 +102,8 @@ __device__ __noinline__ void order_picks_f64(const RouteShape& a, const L* __res
   int rank = 0;
   for (int j = 0; j < count; ++j) {
     const double o = __shfl_sync(kFull, key, j);
-    const int oe = __shfl_sync(kFull, p.x, j);
-    rank += (o > key || (o == key && oe < p.x)) ? 1 : 0;
+    const int oe = __shfl_sync(kFull, e, j);
+    rank += (o > key || (o == key && oe < e)) ? 1 : 0;
   }
   __syncwarp();
   if (lane < count) picks[rank] = p;
@@ -250,18 +256,19 @@ constexpr int kRouteWarps = 4;
 constexpr int kPickRow = kMaxK + 2;
 
 // 4 tokens per warp, 8 lanes per token (`sub` of `tok`).
-//   1  the warp forms one token's keys after another (lanes own 4 experts
-//      each) and leaves them in shared memory
+//   1  the 8 lanes read their token's row, 128 bytes at a time, form the keys
+//      and leave them in shared memory
 //   2  lane `sub` scans the groups sub, sub + 8, ..: two largest, score; the
 //      groups are ranked by counting the better ones
 //   3  the chosen groups' experts are dealt out to the 8 lanes in ascending
-//      order; the maximum of each 4 experts sits in a register, and a round
-//      of the top-k is the maximum over a lane's registers, three shuffles,
-//      and the winner's new block maximum
+//      order; each 4 experts' keys sit sorted in registers, and a round of the
+//      top-k is the maximum over a lane's heads, three shuffles, and the
+//      winner's list moved up; which expert a key belongs to is looked up
+//      after the rounds
 //   4  weights
 // NB: blocks of 4 experts of a lane in step 3, rounded up to a power of two.
 template <typename L, int NB, bool VEC>
-__global__ void __launch_bounds__(32 * kRouteWarps, 8)
+__global__ void __launch_bounds__(32 * kRouteWarps, 7)
 route_kernel(const RouteShape a, const L* __restrict__ logits, const float* __restrict__ bias,
              const uint8_t* __restrict__ mask, int32_t* __restrict__ topk_idx,
              float* __restrict__ topk_w) {
@@ -270,97 +277,96 @@ route_kernel(const RouteShape a, const L* __restrict__ logits, const float* __re
   extern __shared__ __align__(16) float smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane & 7, tok = lane >> 3;
-  const int ROW = 36 * ((a.E + 31) / 32);    // floats of a token's keys
-  float* keys = smem + warp * (4 * ROW + 8 * kPickRow);
+  const int nb = (a.E + 31) >> 5;
+  const int ROW = 36 * nb;                   // floats of a token's keys
+  float* sbias = smem;                       // laid out as a row of keys
+  float* keys = smem + ROW + warp * (4 * ROW + 8 * kPickRow);
   int2* picks = reinterpret_cast<int2*>(keys + 4 * ROW) + tok * kPickRow;
-  const int t0 = (blockIdx.x * (blockDim.x >> 5) + warp) * 4;
-  if (t0 >= a.T) return;
   const float ninf = -INFINITY;
   // what is compared in fp32: the logits themselves where the keys' order is
   // theirs (no bias), else the biased keys
   const bool biased = bias != nullptr;
   const bool by_score = a.space == 1 && biased;   // keys = s + bias
-  unsigned slow = 0;                              // byte r, not 0: token r by fp64 as a whole
-  unsigned live = 0;
-  float row_m = 0.f, row_inv = 1.f;               // softmax of this lane's token
-  const int padded = (a.E + 31) & ~31;
+  if (biased) {
+    for (int e = threadIdx.x; e < 32 * nb; e += blockDim.x) {
+      float v = 0.f;
+      if (e < a.E) {
+        v = bias[e];
+        if (!(v == v)) v = ninf;                  // a NaN switches the expert off
+      }
+      sbias[at(e)] = v;
+    }
+    __syncthreads();
+  }
+  const int t0 = (blockIdx.x * (blockDim.x >> 5) + warp) * 4;
+  if (t0 >= a.T) return;
+  const int t = t0 + tok;
   // ---------------------------------------------------------------- 1 keys
-  float b[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int e = 4 * lane + 128 * (i >> 2) + (i & 3);
-    b[i] = 0.f;
-    if (biased && e < a.E) {
-      b[i] = bias[e];
-      if (!(b[i] == b[i])) b[i] = ninf;           // a NaN switches the expert off
-    }
-  }
+  const bool on = t < a.T && (mask == nullptr || mask[t] != 0);
+  float row_m = 0.f, row_inv = 1.f;               // softmax of this lane's token
+  bool odd = false;                               // values only fp64 decides
   {
-    const bool on = lane < 4 && t0 + lane < a.T && (mask == nullptr || mask[t0 + lane] != 0);
-    live = __ballot_sync(kFull, on);
-  }
-#pragma unroll 1
-  for (int r2 = 0; r2 < 4; r2 += 2) {
-    float4 lv[2][2];
+    const L* row = logits + static_cast<size_t>(t) * a.ld;
+    float4 l[8];
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const L* row = logits + static_cast<size_t>(t0 + r2 + q) * a.ld;
-      const bool on = (live >> (r2 + q)) & 1u;
+    for (int i = 0; i < 8; ++i) {
+      const int e = 4 * sub + 32 * i;
+      l[i] = make_float4(ninf, ninf, ninf, ninf);
+      if (i < nb && on && e < a.E) l[i] = load4<L, VEC>(row, e, a.E);
+    }
+    if (a.gate == 0) {
+      float m = ninf, s = 0.f;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int e = 4 * lane + 128 * i;
-        lv[q][i] = make_float4(ninf, ninf, ninf, ninf);
-        if (on && e < a.E) lv[q][i] = load4<L, VEC>(row, e, a.E);
-      }
+      for (int i = 0; i < 8; ++i)
+        if (i < nb) m = fmaxf(fmaxf(m, fmaxf(l[i].x, l[i].y)), fmaxf(l[i].z, l[i].w));
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+      row_m = m;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < nb)
+          s += (fast_exp(l[i].x - m) + fast_exp(l[i].y - m)) +
+               (fast_exp(l[i].z - m) + fast_exp(l[i].w - m));
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+      odd = !(s >= 0.5f && s <= 1024.f);          // NaN, +inf, or no finite logit
+      row_inv = rcp_approx(s);
     }
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int r = r2 + q;
-      if (!((live >> r) & 1u)) continue;          // warp-uniform
-      float* l = reinterpret_cast<float*>(lv[q]);
-      bool odd = false;                           // values only fp64 decides
-      if (a.gate == 0) {
-        float m = ninf, s = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = fmaxf(m, l[i]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-        float x[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[i] = fast_exp(l[i] - m);
-          s += x[i];
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
-        odd = !(s >= 0.5f && s <= 1024.f);        // NaN, +inf, or no finite logit
-        const float inv = rcp_approx(s);
-        if (tok == r) { row_m = m; row_inv = inv; }
+    for (int i = 0; i < 8; ++i) {
+      if (i >= nb) break;
+      float* v = reinterpret_cast<float*>(&l[i]);
+      if (biased) {
+        const float4 bq = *reinterpret_cast<const float4*>(sbias + 36 * i + 4 * sub);
+        const float* bv = reinterpret_cast<const float*>(&bq);
         if (by_score) {
+          if (a.gate == 0) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) l[i] = l[i] > ninf ? fmaf(x[i], inv, b[i]) : ninf;
+            for (int c = 0; c < 4; ++c)
+              v[c] = v[c] > ninf ? fmaf(fast_exp(v[c] - row_m), row_inv, bv[c]) : ninf;
+          } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[c] = v[c] > ninf ? fast_sigmoid(v[c]) + bv[c] : ninf;
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            odd = odd || !(v[c] <= 1e30f);        // NaN or +inf
+            v[c] = v[c] > ninf ? v[c] + bv[c] : ninf;
+          }
         }
-      } else if (by_score) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) l[i] = l[i] > ninf ? fast_sigmoid(l[i]) + b[i] : ninf;
       } else {
-        // NaN or +inf; beyond 16 distinct logits may have equal fp64 sigmoids
-        const float most = a.space == 1 ? 16.f : 1e30f;
+        // beyond 16 distinct logits may have equal fp64 sigmoids
+        const float most = a.space == 1 && a.gate == 1 ? 16.f : 1e30f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) odd = odd || !(l[i] <= most);
+        for (int c = 0; c < 4; ++c) odd = odd || !(v[c] <= most);
       }
-      if (biased && !by_score) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) l[i] = l[i] > ninf ? l[i] + b[i] : ninf;
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int e = 4 * lane + 128 * i;
-        if (e < padded) *reinterpret_cast<float4*>(keys + r * ROW + at(e)) = lv[q][i];
-      }
-      if (__any_sync(kFull, odd)) slow |= 0xffu << (8 * r);
+      *reinterpret_cast<float4*>(keys + tok * ROW + 36 * i + 4 * sub) = l[i];
     }
   }
+  const unsigned live = __ballot_sync(kFull, on);         // bytes: tokens
+  // byte r, not 0: token r is decided by fp64 as a whole
+  unsigned slow = __ballot_sync(kFull, odd && on);
   __syncwarp();
   float* mykeys = keys + tok * ROW;
   const int per = a.per;
@@ -461,18 +467,18 @@ route_kernel(const RouteShape a, const L* __restrict__ logits, const float* __re
   }
 
   // --------------------------------------------------------------- 3 top-k
-  const bool alive = ((live >> tok) & 1u) && ((slow >> (8 * tok)) & 0xffu) == 0u;
+  const bool alive = on && ((slow >> (8 * tok)) & 0xffu) == 0u;
   const int total = limited && whole ? a.topk_group * per : a.E;   // experts to choose from
   const int nbr = (total + 31) >> 5;               // blocks of 4 of a lane
-  // where the lane's block i lies in the token's keys; blocks that are not
-  // there point at the first and have no maximum
+  // The lane's blocks: where they lie in the token's keys, and their keys in
+  // descending order (a block that is not there holds none).
   int base[NB];
-  float bm[NB];
+  float h[NB][4];
 #pragma unroll
   for (int i = 0; i < NB; ++i) {
     const int p = 4 * (nbr * sub + i);
     base[i] = 0;
-    bm[i] = ninf;
+    float4 q = make_float4(ninf, ninf, ninf, ninf);
     if (alive && i < nbr && p < total) {
       int e = p;
       if (limited && whole) {
@@ -480,19 +486,25 @@ route_kernel(const RouteShape a, const L* __restrict__ logits, const float* __re
         e = picks[gi].x + p - gi * per;
       }
       base[i] = at(e);
-      const float4 q = *reinterpret_cast<const float4*>(mykeys + base[i]);
-      bm[i] = fmaxf(fmaxf(q.x, q.y), fmaxf(q.z, q.w));
+      q = *reinterpret_cast<const float4*>(mykeys + base[i]);
     }
+    const float x1 = fmaxf(q.x, q.y), x2 = fminf(q.x, q.y);
+    const float y1 = fmaxf(q.z, q.w), y2 = fminf(q.z, q.w);
+    h[i][0] = fmaxf(x1, y1);
+    h[i][3] = fminf(x2, y2);
+    const float u = fminf(x1, y1), v = fmaxf(x2, y2);
+    h[i][1] = fmaxf(u, v);
+    h[i][2] = fminf(u, v);
   }
   __syncwarp();
   const unsigned lower = (0xffu << (tok << 3)) & ((1u << lane) - 1u);   // this token's lower lanes
   int count = 0;
-  // pick j: (place in the token's keys, key).  Written without branches: the
-  // four tokens' winners sit at different places.
+  // pick j: (place of its block, key).  Without branches: the four tokens'
+  // winners sit at different places.
   auto round = [&](int j) {
-    float lm = bm[0];
+    float lm = h[0][0];
 #pragma unroll
-    for (int i = 1; i < NB; ++i) lm = fmaxf(lm, bm[i]);
+    for (int i = 1; i < NB; ++i) lm = fmaxf(lm, h[i][0]);
     float best = lm;
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(kFull, best, o));
@@ -501,26 +513,42 @@ route_kernel(const RouteShape a, const L* __restrict__ logits, const float* __re
     const unsigned who = __ballot_sync(kFull, lm == best);
     const bool win = any && lm == best && (who & lower) == 0u;
     count += any ? 1 : 0;
-    int ix = base[NB - 1];
+    bool open = win;
+    int place = 0;
 #pragma unroll
-    for (int i = NB - 2; i >= 0; --i) ix = bm[i] == best ? base[i] : ix;
-    const float4 q = *reinterpret_cast<const float4*>(mykeys + ix);
-    int c = q.z == best ? 2 : 3;
-    c = q.y == best ? 1 : c;
-    c = q.x == best ? 0 : c;
-    const float nm = fmaxf(fmaxf(c == 0 ? ninf : q.x, c == 1 ? ninf : q.y),
-                           fmaxf(c == 2 ? ninf : q.z, c == 3 ? ninf : q.w));
-    if (win) {
-      picks[j] = make_int2(ix + c, __float_as_int(best));
-      mykeys[ix + c] = ninf;
+    for (int i = 0; i < NB; ++i) {
+      const bool hit = open && h[i][0] == best;
+      open = open && !hit;
+      place = hit ? base[i] : place;
+      h[i][0] = hit ? h[i][1] : h[i][0];
+      h[i][1] = hit ? h[i][2] : h[i][1];
+      h[i][2] = hit ? h[i][3] : h[i][2];
+      h[i][3] = hit ? ninf : h[i][3];
     }
-#pragma unroll
-    for (int i = 0; i < NB; ++i) bm[i] = win && base[i] == ix ? nm : bm[i];
+    if (win) picks[j] = make_int2(place, __float_as_int(best));
+  };
+  // The expert of pick j: the first in its block with that key, or as many
+  // further as earlier picks share block and key.  Kept beside the place
+  // (bits 16 and 17), which other lanes may still be reading.
+  auto resolve = [&](int j) {
+    const int2 p = picks[j];
+    const float key = __int_as_float(p.y);
+    const float4 q = *reinterpret_cast<const float4*>(mykeys + p.x);
+    unsigned eq = (q.x == key ? 1u : 0u) | (q.y == key ? 2u : 0u) | (q.z == key ? 4u : 0u) |
+                  (q.w == key ? 8u : 0u);
+    if (eq & (eq - 1u)) {
+      for (int i = 0; i < j; ++i) {
+        const int2 o = picks[i];
+        if ((o.x & 0xffff) == p.x && __int_as_float(o.y) == key) eq &= eq - 1u;   // -0 is 0
+      }
+    }
+    picks[j].x = p.x | ((__ffs(eq) - 1) << 16);
   };
   for (int j = 0; j <= a.k; ++j) round(j);   // one more than k: is the last one's lead clear
   __syncwarp();
+  for (int j = sub; j < count; j += 8) resolve(j);
+  __syncwarp();
   // the logit of the lane's first pick, asked for before it is needed
-  const int t = t0 + tok;
   float first = 0.f;
   bool moved = false;
   if (biased && sub < count)
@@ -554,6 +582,8 @@ route_kernel(const RouteShape a, const L* __restrict__ logits, const float* __re
         const int before = count;
         round(a.k + 1);
         __syncwarp();
+        if (count > before && sub == 0) resolve(before);
+        __syncwarp();
         again = __ballot_sync(kFull, edge && count > before && close(a.k));
         // (a tie further down: the whole token in fp64)
       }
@@ -569,8 +599,7 @@ route_kernel(const RouteShape a, const L* __restrict__ logits, const float* __re
       }
     }
   }
-  // padding tokens are not decided at all
-  slow &= 0xffu * ((live & 1u) | (live & 2u) << 7 | (live & 4u) << 14 | (live & 8u) << 21);
+  slow &= live;   // padding tokens are not decided at all
 
   // ------------------------------------------------------------- 4 weights
   const int n = count < a.k ? count : a.k;
@@ -830,8 +859,8 @@ cudaError_t route_launch(const RouteShape& a, const L* logits, const float* bias
   // one warp per block until there are enough tokens for four on every SM
   const int warps = a.T <= 148 * 16 ? 1 : kRouteWarps;
   const unsigned grid = static_cast<unsigned>((a.T + 4 * warps - 1) / (4 * warps));
-  const size_t smem = static_cast<size_t>(warps) *
-                      (4 * 36 * ((a.E + 31) / 32) + 8 * kPickRow) * sizeof(float);
+  const size_t row = 36 * ((a.E + 31) / 32);   // floats of a token's keys, and of the bias
+  const size_t smem = (row + warps * (4 * row + 8 * kPickRow)) * sizeof(float);
   const bool vec = a.E % 4 == 0 && a.ld % 4 == 0 &&
                    (reinterpret_cast<uintptr_t>(logits) & (4 * sizeof(L) - 1)) == 0;
   const int per = a.per;

@@ -135,6 +135,17 @@ def test_routing_ties_and_near_ties(gate, space):
                norm=False)
 
 
+def test_routing_signed_zeros():
+    """-0 and 0 are equal: each expert once, in the order of their ids."""
+    l = torch.zeros(8, 64, device="cuda")
+    l[:, ::3] = -0.0
+    l[:, 40:] = -1.0
+    for bias in (None, torch.zeros(64, device="cuda")):
+        for space in (0, 1):
+            _check(l, 20, space=space, bias=bias, groups=4, topk_group=3, score=1)
+            _check(l, 32, space=space, bias=bias)
+
+
 @pytest.mark.parametrize("gate", [SIG, SOFT])
 @pytest.mark.parametrize("space", [0, 1])
 @pytest.mark.parametrize("score", [1, 2])
