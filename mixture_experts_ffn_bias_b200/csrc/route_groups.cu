@@ -11,10 +11,11 @@
 //   the topk_group best groups stay, then the top_k best of their experts;
 //   w = scale s / (sum of the chosen s + 1e-9), or scale s.
 // The selection is the one fp64 keys give, ties to the lower id.  Keys are
-// compared in fp32 first.  Picks whose keys are closer than their fp32 error
-// are put in order by fp64 keys of theirs alone (a few tokens in a thousand);
-// a token whose groups are that close, or with values fp32 cannot rank, is
-// decided again as a whole in fp64.
+// compared in fp32 first.  Groups, and picks, whose fp32 values are closer than
+// their error are put in order by fp64 values of theirs alone (a few tokens
+// in a thousand; deciding such a token anew as a whole, 10 us, showed as the
+// tail of every launch); a token with values fp32 cannot rank is decided
+// again as a whole in fp64.
 //
 // Bound by memory for many tokens (the logits are read once), by the
 // selection's instructions close behind: 4 tokens per warp, 8 lanes each, so
@@ -65,19 +66,89 @@ __device__ __forceinline__ unsigned long long ordered(double v) {
   return static_cast<unsigned long long>(b < 0 ? ~b : b | (1ll << 63));
 }
 
-// The fp64 score of a logit of a row: (m, sum) of the softmax, by one warp.
+// The softmax of a row in fp64, by one warp: its maximum, the divisor, and
+// e^(l - m) of the lane's experts lane + 32 i.  All loads, then all exponentials
+// are in flight together: this runs for single tokens, where latency counts.
 template <typename L>
 __device__ __forceinline__ void softmax_f64(const RouteShape& a, const L* __restrict__ row,
-                                            int lane, double& m, double& sum) {
-  m = -INFINITY;
-  for (int e = lane; e < a.E; e += 32) m = fmax(m, to_f64(row[e]));
+                                            int lane, double& m, double& sum, double (&x)[8]) {
+  double l[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    l[i] = lane + 32 * i < a.E ? to_f64(row[lane + 32 * i]) : -INFINITY;
+  m = l[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = fmax(m, l[i]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(kFull, m, o));
   if (m == -INFINITY) m = 0.0;
-  sum = 0.0;
-  for (int e = lane; e < a.E; e += 32) sum += exp(to_f64(row[e]) - m);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = exp(l[i] - m);   // 0 past E
+  sum = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+}
+
+// The fp64 key of expert e (-inf where it is not eligible).
+template <typename L>
+__device__ __forceinline__ double key_f64(const RouteShape& a, const L* __restrict__ row,
+                                          const float* __restrict__ bias, int e, double m,
+                                          double sum) {
+  const double l = to_f64(row[e]);
+  double key = l;
+  if (a.space == 1) {
+    const double x = exp(a.gate == 0 ? l - m : -l);
+    key = a.gate == 0 ? x / sum : 1.0 / (1.0 + x);
+  }
+  if (bias != nullptr) key += static_cast<double>(bias[e]);
+  return l > -INFINITY && key > -INFINITY ? key : -INFINITY;
+}
+
+// The two largest of (m1 >= m2) and another pair.
+__device__ __forceinline__ void top2(double& m1, double& m2, double o1, double o2) {
+  m2 = fmax(fmin(m1, o1), fmax(m2, o2));
+  m1 = fmax(m1, o1);
+}
+
+// The groups of one token whose fp32 scores (picks: error, score) overlap the
+// border [lo, hi] between the chosen and the others, by fp64 scores; returns the
+// chosen groups.  By the whole warp: one group after another.
+template <typename L>
+__device__ __noinline__ unsigned choose_groups_f64(const RouteShape& a, const L* __restrict__ row,
+                                                   const float* __restrict__ bias, int lane,
+                                                   float lo, float hi, const int2* picks) {
+  double m = 0.0, sum = 1.0;
+  if (a.gate == 0 && a.space == 1) {
+    double x[8];
+    softmax_f64(a, row, lane, m, sum, x);
+  }
+  bool open = false, in = false;
+  if (lane < a.groups) {
+    const float err = __int_as_float(picks[lane].x), sc = __int_as_float(picks[lane].y);
+    open = sc > -INFINITY && sc + err >= lo && sc - err <= hi;
+    in = sc > -INFINITY && sc - err > hi;
+  }
+  const unsigned todo = __ballot_sync(kFull, open);
+  unsigned chosen = __ballot_sync(kFull, in);
+  double score = -INFINITY;
+  for (unsigned g = todo; g != 0u; g &= g - 1u) {
+    const int gi = __ffs(g) - 1;
+    double m1 = -INFINITY, m2 = -INFINITY;
+    for (int e = lane; e < a.per; e += 32)
+      top2(m1, m2, key_f64(a, row, bias, gi * a.per + e, m, sum), -INFINITY);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      top2(m1, m2, __shfl_xor_sync(kFull, m1, o), __shfl_xor_sync(kFull, m2, o));
+    if (lane == gi) score = a.group_score == 2 && m2 > -INFINITY ? m1 + m2 : m1;
+  }
+  int rank = __popc(chosen);
+  for (unsigned g = todo; g != 0u; g &= g - 1u) {
+    const int h = __ffs(g) - 1;
+    const double o = __shfl_sync(kFull, score, h);
+    rank += (o > score || (o == score && h < lane)) ? 1 : 0;
+  }
+  chosen |= __ballot_sync(kFull, open && rank < a.topk_group);
+  return chosen;
 }
 
 // The `count` <= 32 best experts of one token by fp32 keys (picks: position,
@@ -88,16 +159,17 @@ __device__ __noinline__ void order_picks_f64(const RouteShape& a, const L* __res
                                              const float* __restrict__ bias, int lane, int count,
                                              int2* picks) {
   double m = 0.0, sum = 1.0;
-  if (a.gate == 0 && a.space == 1) softmax_f64(a, row, lane, m, sum);
+  if (a.gate == 0 && a.space == 1) {
+    double x[8];
+    softmax_f64(a, row, lane, m, sum, x);
+  }
   int2 p = make_int2(0, 0);
   double key = -INFINITY;
   int e = kMaxE;
   if (lane < count) {
     p = picks[lane];
     e = expert_at(p.x);
-    key = to_f64(row[e]);
-    if (a.space == 1) key = a.gate == 0 ? exp(key - m) / sum : 1.0 / (1.0 + exp(-key));
-    if (bias != nullptr) key += static_cast<double>(bias[e]);
+    key = key_f64(a, row, bias, e, m, sum);
   }
   int rank = 0;
   for (int j = 0; j < count; ++j) {
@@ -118,66 +190,73 @@ __device__ __noinline__ void route_token_f64(const RouteShape& a, const L* __res
                                              float* __restrict__ topk_w) {
   const double ninf = -INFINITY;
   double m = 0.0, sum = 1.0;
-  if (a.gate == 0) softmax_f64(a, row, lane, m, sum);
-  auto score = [&](double l) {
-    return a.gate == 0 ? exp(l - m) / sum : 1.0 / (1.0 + exp(-l));
-  };
-  for (int e = lane; e < a.E; e += 32) {
-    const double l = to_f64(row[e]);
-    const double s = score(l);
-    double key = a.space == 1 ? s : l;
-    if (bias != nullptr) key += static_cast<double>(bias[e]);
-    const bool ok = l > ninf && s == s && key > ninf;
-    skey[e] = ok ? key : ninf;
+  double key[8];                           // of the experts lane + 32 i
+  if (a.gate == 0) {
+    softmax_f64(a, row, lane, m, sum, key);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) key[i] /= sum;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      key[i] = lane + 32 * i < a.E ? 1.0 / (1.0 + exp(-to_f64(row[lane + 32 * i]))) : 0.0;
   }
-  __syncwarp();
-  const int per = a.per;
-  unsigned use = kFull;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int e = lane + 32 * i;
+    const double l = e < a.E ? to_f64(row[e]) : ninf;
+    const bool ok = l > ninf && key[i] == key[i];
+    if (a.space == 0) key[i] = l;
+    if (bias != nullptr && e < a.E) key[i] += static_cast<double>(bias[e]);
+    key[i] = ok && key[i] > ninf ? key[i] : ninf;
+  }
   if (a.topk_group < a.groups) {
-    double sc = ninf;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (lane + 32 * i < a.E) skey[lane + 32 * i] = key[i];
+    __syncwarp();
+    double m1 = ninf, m2 = ninf;
     if (lane < a.groups) {
-      double m1 = ninf, m2 = ninf;
-      for (int e = lane * per; e < (lane + 1) * per; ++e) {
-        const double v = skey[e];
-        if (v > m1) { m2 = m1; m1 = v; } else if (v > m2) { m2 = v; }
-      }
-      sc = a.group_score == 2 && m2 > ninf ? m1 + m2 : m1;
+#pragma unroll 8
+      for (int e = lane * a.per; e < (lane + 1) * a.per; ++e) top2(m1, m2, skey[e], ninf);
     }
+    const double sc = a.group_score == 2 && m2 > ninf ? m1 + m2 : m1;
     int rank = 0;
     for (int h = 0; h < a.groups; ++h) {
       const double o = __shfl_sync(kFull, sc, h);
       rank += (o > sc || (o == sc && h < lane)) ? 1 : 0;
     }
-    use = __ballot_sync(kFull, lane < a.groups && rank < a.topk_group);
+    const unsigned use = __ballot_sync(kFull, lane < a.groups && rank < a.topk_group);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (lane + 32 * i < a.E && !((use >> ((lane + 32 * i) / a.per)) & 1u)) key[i] = ninf;
+    __syncwarp();
   }
-  // each lane's best expert as an ordered integer; only the round's winner
-  // looks again
-  int mine = -1, be = kMaxE;
-  unsigned long long ob = 0;
-  auto look = [&]() {
-    double best = ninf;
-    be = kMaxE;
-    for (int e = lane; e < a.E; e += 32) {
-      const double v = skey[e];
-      if (v > best && ((use >> (a.topk_group < a.groups ? e / per : 0)) & 1u)) { best = v; be = e; }
-    }
-    ob = be < kMaxE ? ordered(best) : 0ull;
-  };
-  look();
+  // a round: each lane's best as an ordered integer
+  int mine = -1;
   for (int j = 0; j < a.k; ++j) {
+    double best = ninf;
+    int bi = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (key[i] > best) { best = key[i]; bi = i; }
+    const unsigned long long ob = best > ninf ? ordered(best) : 0ull;
     const unsigned h = static_cast<unsigned>(ob >> 32);
     const unsigned mh = __reduce_max_sync(kFull, h);
     if (mh == 0u) break;                 // nothing eligible is left
     const unsigned l = h == mh ? static_cast<unsigned>(ob) : 0u;
     const unsigned ml = __reduce_max_sync(kFull, l);
+    const int be = lane + 32 * bi;
     const int e = __reduce_min_sync(kFull, h == mh && l == ml ? be : kMaxE);
     if (lane == j) mine = e;
-    if (be == e) {
-      skey[e] = ninf;
-      look();
-    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (lane + 32 * i == e) key[i] = ninf;
   }
-  double s = mine >= 0 ? score(to_f64(row[mine])) : 0.0;
+  double s = 0.0;
+  if (mine >= 0) {
+    const double x = exp(a.gate == 0 ? to_f64(row[mine]) - m : -to_f64(row[mine]));
+    s = a.gate == 0 ? x / sum : 1.0 / (1.0 + x);
+  }
   double tot = s;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(kFull, tot, o);
@@ -253,7 +332,8 @@ __device__ __forceinline__ float4 load4(const L* __restrict__ row, int e, int E)
 }
 
 constexpr int kRouteWarps = 4;
-constexpr int kPickRow = kMaxK + 2;
+constexpr int kMorePicks = 8;   // looked at where the last chosen one's lead is not clear
+constexpr int kPickRow = kMaxK + 2 + kMorePicks;
 
 // 4 tokens per warp, 8 lanes per token (`sub` of `tok`).
 //   1  the 8 lanes read their token's row, 128 bytes at a time, form the keys
@@ -369,10 +449,15 @@ route_kernel(const RouteShape a, const L* __restrict__ logits, const float* __re
   unsigned slow = __ballot_sync(kFull, odd && on);
   __syncwarp();
   float* mykeys = keys + tok * ROW;
+  // A score's fp32 error: 2.5e-7 of a sigmoid; of a softmax, whose largest
+  // term is row_inv, 9e-7 row_inv (the exponential 4e-7, the divisor 5e-7).  The
+  // sum with the bias rounds once more, 2^-24 of the key.
+  const float key_err = !by_score ? 0.f : a.gate == 0 ? 9e-7f * row_inv : 2.5e-7f;
   const int per = a.per;
   const bool limited = a.topk_group < a.groups;
   const bool whole = (per & 3) == 0;              // groups are whole blocks of 4
   const float inv_per = rcp_approx(static_cast<float>(per));   // of small integers only
+  unsigned use = kFull;                           // groups this lane's token may use
   // -------------------------------------------------------------- 2 groups
   if (limited) {
     // a score's fp32 error: none for the largest of unbiased logits, relative
@@ -408,17 +493,17 @@ route_kernel(const RouteShape a, const L* __restrict__ logits, const float* __re
             err = 1e-5f * sc;
           } else {
             sc = fast_sigmoid(m1) + (two ? fast_sigmoid(m2) : 0.f);
-            err = 1.2e-6f;
+            err = 7e-7f;
           }
         }
       } else if (biased || two) {
         if (two) sc = m1 + m2;
-        err = 1.2e-6f + 2e-7f * (fabsf(m1) + (two ? fabsf(m2) : 0.f));
+        err = 2.f * key_err + 1.5e-7f * (fabsf(m1) + (two ? fabsf(m2) : 0.f));
       }
       picks[g] = make_int2(__float_as_int(err), __float_as_int(sc));
     }
     __syncwarp();
-    unsigned use = 0;
+    use = 0;
     float lo = INFINITY, hi = ninf;
 #pragma unroll 1
     for (int i = 0; 8 * i < a.groups; ++i) {
@@ -446,12 +531,29 @@ route_kernel(const RouteShape a, const L* __restrict__ logits, const float* __re
     bool near = hi > ninf && !(lo > hi);
     if (!biased && a.group_score == 1) {
       // largest logits: equal ones are equal keys and the lower group is
-      // right; close ones, and ones whose scores leave fp64, may be equal
-      // as scores only
+      // right; others may be equal as fp64 scores next to zero, and where
+      // the scores leave fp64's range
       near = a.space == 1 && hi > ninf &&
-             ((lo > hi && lo - hi < 1e-7f) || lo < (a.gate == 0 ? row_m - 700.f : -700.f));
+             ((lo - hi <= 1e-12f && fabsf(lo) < 1e-6f) ||
+              lo < (a.gate == 0 ? row_m - 700.f : -700.f));
     }
-    slow |= __ballot_sync(kFull, near);           // (the shuffles were warp barriers)
+    const unsigned close_calls = __ballot_sync(kFull, near) & live & ~slow;
+    if (close_calls != 0u) {                      // warp-uniform
+      if (!biased && a.group_score == 1) {
+        slow |= close_calls;                      // differences fp32 logits do not show
+      } else {
+#pragma unroll 1
+        for (int r = 0; r < 4; ++r) {
+          if (!((close_calls >> (8 * r)) & 0xffu)) continue;
+          const unsigned u = choose_groups_f64<L>(
+              a, logits + static_cast<size_t>(t0 + r) * a.ld, bias, lane,
+              __shfl_sync(kFull, lo, 8 * r), __shfl_sync(kFull, hi, 8 * r),
+              picks + (r - tok) * kPickRow);
+          if (tok == r) use = u;
+        }
+      }
+    }
+    __syncwarp();                                 // the scores have been read
     if (whole) {
       // the chosen groups in ascending order
 #pragma unroll 1
@@ -555,37 +657,75 @@ route_kernel(const RouteShape a, const L* __restrict__ logits, const float* __re
     first = to_f32<L>(logits[static_cast<size_t>(t) * a.ld + expert_at(picks[sub].x)]);
   // ---------------------------------------------- are the leads clear in fp32
   if (biased || a.space == 1) {
-    // whether picks j and j + 1 are
-    auto close = [&](int j) {
+    const L* row = logits + static_cast<size_t>(t) * a.ld;
+    // Keys closer than this may be in the wrong order.  Without a bias they are
+    // the logits: distinct ones have distinct fp64 scores, but next to zero
+    // (below 1e-15 apart) and below `floor`, where the scores leave fp64's range.
+    auto margin = [&](float key) {
+      return biased ? 2.f * key_err + 2e-7f * (fabsf(key) + 1e-3f) : 1e-12f;
+    };
+    const float floor = biased ? ninf : a.gate == 0 ? row_m - 700.f : -700.f;
+    // equal inputs make equal keys: an exact tie, ordered by id as it should be
+    auto same = [&](int e, int f) {
+      return to_f32<L>(row[e]) == to_f32<L>(row[f]) && bias[e] == bias[f];
+    };
+    bool near = false;   // two neighbours of the chosen ones
+    bool edge = false;   // the last of them and the best one left out
+    for (int j = sub; j + 1 < count; j += 8) {
       const int2 p = picks[j], n = picks[j + 1];
       const float best = __int_as_float(p.y), gap = best - __int_as_float(n.y);
-      if (!biased)
-        return (gap > 0.f && gap < 1e-7f) || best < (a.gate == 0 ? row_m - 700.f : -700.f);
-      if (gap > 1.5e-6f + 2.5e-7f * fabsf(best)) return false;
-      // keys formed in fp32; equal inputs are an exact tie
-      const L* row = logits + static_cast<size_t>(t0 + tok) * a.ld;
-      const int e = expert_at(p.x), f = expert_at(n.x);
-      return !(to_f32<L>(row[e]) == to_f32<L>(row[f]) && bias[e] == bias[f]);
-    };
-    bool near = false, edge = false;
-    for (int j = sub; j + 1 < count; j += 8)
-      if (close(j)) {
-        near = true;
-        edge = edge || j + 1 == a.k;
-      }
-    unsigned fix = __ballot_sync(kFull, near);
-    if (fix != 0u) {   // warp-uniform
+      const bool c = !(gap > margin(best)) || best < floor;
+      if (j + 1 == a.k)
+        edge = c && (biased || fabsf(best) < 1e-6f || best < floor);
+      else if (c)
+        near = near || (biased ? !same(expert_at(p.x), expert_at(n.x)) : gap > 0.f);
+    }
+    if (__any_sync(kFull, near || edge)) {
       moved = true;
-      unsigned again = 0;
-      if (__any_sync(kFull, edge)) {
-        // the best one left out is as close: is the next one clear
-        const int before = count;
-        round(a.k + 1);
-        __syncwarp();
-        if (count > before && sub == 0) resolve(before);
-        __syncwarp();
-        again = __ballot_sync(kFull, edge && count > before && close(a.k));
-        // (a tie further down: the whole token in fp64)
+      const unsigned edges = __ballot_sync(kFull, edge);
+      bool open = ((edges >> (8 * tok)) & 0xffu) != 0u;
+      unsigned fix = __ballot_sync(kFull, near), again = 0;
+      if (edges != 0u) {
+        const int2 last = open ? picks[a.k - 1] : make_int2(0, 0);
+        const float lk = __int_as_float(last.y);
+        if (open) {
+          // is any expert that close to the last chosen one not an exact tie
+          // with it (it may be hidden behind ties)
+          bool differs = false;
+          for (int e = 4 * sub; e < a.E; e += 32) {
+            if (limited && whole && !((use >> static_cast<int>((e + 0.5f) * inv_per)) & 1u))
+              continue;
+            const float4 q = *reinterpret_cast<const float4*>(mykeys + at(e));
+            const float v[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (biased)
+                differs = differs || (fabsf(v[c] - lk) <= margin(lk) &&
+                                      !same(e + c, expert_at(last.x)));
+              else
+                differs = differs || (v[c] != lk && v[c] > ninf &&
+                                      (fabsf(v[c] - lk) <= margin(lk) ||
+                                       (lk < floor && v[c] < floor)));
+          }
+          open = differs;
+        }
+        const unsigned any = __ballot_sync(kFull, open);
+        open = ((any >> (8 * tok)) & 0xffu) != 0u;
+        fix |= any;
+        // the next ones, until one is clearly behind
+#pragma unroll 1
+        for (int x = 1; x <= kMorePicks && __any_sync(kFull, open); ++x) {
+          const int before = count;
+          round(a.k + x);
+          __syncwarp();
+          if (count > before && sub == 0) resolve(before);
+          __syncwarp();
+          if (open) {
+            const float next = __int_as_float(picks[before].y);
+            open = count > before && (!(lk - next > margin(lk)) || next < floor);
+          }
+        }
+        again = __ballot_sync(kFull, open);
       }
       const unsigned many = __ballot_sync(kFull, count > 32);
 #pragma unroll 1

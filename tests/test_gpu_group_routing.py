@@ -135,6 +135,30 @@ def test_routing_ties_and_near_ties(gate, space):
                norm=False)
 
 
+@pytest.mark.parametrize("gate", [SIG, SOFT])
+def test_routing_many_ties_at_the_border(gate):
+    """Exact ties of the last chosen expert hide others whose keys differ by less
+    than fp32 shows; logits so near zero that their fp64 scores are equal;
+    and tokens whose logits are all equal."""
+    T, E, k = 64, 128, 8
+    rng = np.random.default_rng(12)
+    l = np.full((T, E), 0.7, np.float32)
+    up = rng.uniform(size=(T, E)) < 0.2
+    l[up] = np.nextafter(np.float32(0.7), np.float32(1))
+    l[:, ::7] = -1.0
+    tiny = (rng.integers(0, 3, E) * 2e-8).astype(np.float32)
+    small = (rng.integers(-2, 3, (T, E)) * 1e-18).astype(np.float32)
+    flat = np.zeros((T, E), np.float32)
+    for a in (l, small, flat):
+        for b in (None, np.zeros(E, np.float32), tiny):
+            for space in (0, 1):
+                for groups, tg in ((1, 1), (8, 3)):
+                    for score in (1, 2):
+                        _check(torch.from_numpy(a).cuda(), k, gate=gate, space=space,
+                               bias=None if b is None else torch.from_numpy(b).cuda(),
+                               groups=groups, topk_group=tg, score=score)
+
+
 def test_routing_signed_zeros():
     """-0 and 0 are equal: each expert once, in the order of their ids."""
     l = torch.zeros(8, 64, device="cuda")
