@@ -256,6 +256,50 @@ def test_routing_many_tokens_match_the_fp64_selection():
         assert torch.all((w.double() - rw).abs() <= W_RTOL * rw)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_routing_layouts_streams_and_graphs(dtype):
+    """Rows at odd offsets and strides give what dense ones give; captured and
+    replayed on new logits; two calls at once on two streams."""
+    T, E, k = 333, 64, 6
+    base = _logits(T, E + 9, 31, dtype)
+    views = [base[:, 1:E + 1], base[:, 4:E + 4], base[:, 8:E + 8]]
+    kw = dict(groups=8, topk_group=3, bias=0.1 * torch.rand(E, device="cuda"))
+    for v in views:
+        cfg, o, i0, w0 = _route(v, k, **kw)
+        _, _, i1, w1 = _route(v.contiguous(), k, **kw)
+        assert torch.equal(i0, i1) and torch.equal(w0, w1)
+        dw = torch.randn(T, k, device="cuda")
+        a = torch.zeros(T, E + 3, dtype=dtype, device="cuda")
+        b = torch.empty(T, E, dtype=dtype, device="cuda")
+        B.moe_route_groups_backward(cfg, o, v, i0, dw, a[:, 1:E + 1])
+        B.moe_route_groups_backward(cfg, o, v.contiguous(), i0, dw, b)
+        assert torch.equal(a[:, 1:E + 1], b) and torch.all(a[:, 0] == 0)
+    l, idx, w = views[1].contiguous(), torch.empty_like(i0), torch.empty_like(w0)
+    dl = torch.empty_like(l)
+    B.moe_route_groups(cfg, o, l, kw["bias"], None, idx, w)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        B.moe_route_groups(cfg, o, l, kw["bias"], None, idx, w)
+        B.moe_route_groups_backward(cfg, o, l, idx, w, dl)
+    for v in (views[0], views[2]):
+        l.copy_(v)
+        graph.replay()
+        torch.cuda.synchronize()
+        _, _, i1, w1 = _route(v, k, **kw)
+        d1 = torch.empty_like(dl)
+        B.moe_route_groups_backward(cfg, o, v, i1, w1, d1)
+        assert torch.equal(idx, i1) and torch.equal(w, w1) and torch.equal(dl, d1)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    r1 = [_route(views[0], k, stream=s1, **kw) for _ in range(3)]
+    r2 = [_route(views[2], k, stream=s2, **kw) for _ in range(3)]
+    torch.cuda.synchronize()
+    for r, v in ((r1, views[0]), (r2, views[2])):
+        _, _, i1, w1 = _route(v, k, **kw)
+        assert all(torch.equal(x[2], i1) and torch.equal(x[3], w1) for x in r)
+
+
 # ----------------------------------------------------------------- gradient
 @pytest.mark.parametrize("case", CASES, ids=str)
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
@@ -367,6 +411,47 @@ def test_orthogonalize_matches_the_oracle(shape, din, dout):
     out, ws = _ortho(g, dout)
     assert B.moe_device_status(ws) == (B.MOE_OK, 0)
     assert _ortho_err(out, g) <= O_TOL[dout]
+
+
+def _ref64(g, steps=5, coeffs=B.MUON_COEFFS, eps=1e-7):
+    """The oracle's iteration in torch on the GPU, 64 bits, for larger batches."""
+    a, b, c = (float(np.float32(v)) for v in coeffs)
+    x = g.double()
+    tall = x.shape[1] > x.shape[2]
+    x = x.transpose(1, 2) if tall else x
+    x = x / (torch.linalg.vector_norm(x, dim=(1, 2), keepdim=True) + float(np.float32(eps)))
+    for _ in range(steps):
+        A = x @ x.transpose(1, 2)
+        x = a * x + (b * A + c * (A @ A)) @ x
+    return x.transpose(1, 2) if tall else x
+
+
+# every tile shape of every product, with and without mirrored tiles, ragged at
+# their edges; rows below 64 that do not fit one launch; widths from one to
+# sixteen CTAs of the one-launch kernel, four boxes a CTA, and both orders
+BATCHES = [(20, 400, 400), (9, 510, 510), (64, 250, 287), (64, 250, 250), (3, 900, 900),
+           (40, 400, 805), (20, 700, 700), (9, 330, 331), (40, 130, 130), (6, 805, 400),
+           (2, 40, 2500), (2, 2500, 40), (1, 128, 2048), (1, 1100, 100), (3, 100, 1500),
+           (150, 100, 250), (40, 70, 600), (5, 128, 129), (2, 129, 128), (1, 3, 2048)]
+
+
+@pytest.mark.parametrize("shape", BATCHES, ids=str)
+@pytest.mark.parametrize("dout", [torch.float32, torch.bfloat16])
+def test_orthogonalize_batches(shape, dout):
+    gen = torch.Generator(device="cuda").manual_seed(sum(shape))
+    g = torch.randn(*shape, generator=gen, device="cuda")
+    out, ws = _ortho(g, dout)
+    assert B.moe_device_status(ws) == (B.MOE_OK, 0)
+    ref = _ref64(g)
+    err = torch.linalg.vector_norm(out.double() - ref, dim=(1, 2)) / \
+        torch.linalg.vector_norm(ref, dim=(1, 2))
+    assert err.max().item() <= O_TOL[dout]
+    again, _ = _ortho(g, dout)
+    assert torch.equal(out, again)
+    # a matrix alone gives what it gives in the batch, to the same bound
+    if shape[0] > 1:
+        one, _ = _ortho(g[-1:], dout)
+        assert _ortho_err(one, g[-1:]) <= O_TOL[dout]
 
 
 @pytest.mark.parametrize("dout", [torch.float32, torch.bfloat16])
