@@ -352,10 +352,11 @@ class _Types:
         self.f32, self.i32 = (torch.float32,), (torch.int32,)
         self.mask = (torch.uint8, torch.bool)
         self.of = {DTYPE_F32: (torch.float32,), DTYPE_BF16: (torch.bfloat16,)}
-        self._torch = torch
+        self._ready, self._device = torch.cuda.is_initialized, torch._C._cuda_getDevice
 
     def device(self) -> int:
-        return (self._torch._C._cuda_getDevice() if self._torch.cuda.is_initialized() else -2)
+        """The current CUDA device (-2, like no tensor's, before CUDA is in use)."""
+        return self._device() if self._ready() else -2
 
 
 _types = None
@@ -390,20 +391,14 @@ def make_group_opts(n_group=1, topk_group=1, group_score=2, bias_space=1, scale=
     return MoEGroupOpts(n_group, topk_group, group_score, bias_space, logits_dtype, scale)
 
 
-def _of(c: _Types, opts) -> tuple:
-    return c.of.get(opts.logits_dtype, ())
-
-
-def _logits_ld(t, cfg, what="logits") -> int:
+def _logits_ld(t, T, E, what="logits") -> int:
     """Row stride of a [T, E] tensor whose rows are contiguous."""
-    shape = t.shape
-    if len(shape) != 2 or shape[0] != cfg.T or shape[1] != cfg.n_experts:
-        raise MoEError(MOE_ERR_INVALID,
-                       f"{what} of shape {tuple(t.shape)}, expected {(cfg.T, cfg.n_experts)}")
+    if t.shape != (T, E):
+        raise MoEError(MOE_ERR_INVALID, f"{what} of shape {tuple(t.shape)}, expected {(T, E)}")
     row, col = t.stride()
-    if col != 1 and cfg.n_experts > 1:
+    if col != 1 and E > 1:
         raise MoEError(MOE_ERR_INVALID, f"the elements of a row of {what} must be contiguous")
-    return row if cfg.T > 1 else cfg.n_experts
+    return row if T > 1 else E
 
 
 def moe_route_groups(cfg, opts, logits, sel_bias, token_mask, topk_idx, topk_w, stream=None,
@@ -411,35 +406,33 @@ def moe_route_groups(cfg, opts, logits, sel_bias, token_mask, topk_idx, topk_w, 
     """Group-limited routing of logits [T, E] (rows may be strided); token_mask
     [T] uint8 or bool, 0 for padding, or None."""
     T, E, k = cfg.T, cfg.n_experts, cfg.top_k
-    ld = _logits_ld(logits, cfg)
+    ld = _logits_ld(logits, T, E)
     if T == 0:
         logits = sel_bias = token_mask = topk_idx = topk_w = None
     c = _checks()
     dev = c.device()
-    st = lib().moe_route_groups(ctypes.byref(cfg), ctypes.byref(opts),
-                                _arg(logits, "logits", _of(c, opts), 0, dev, False), ld,
-                                _arg(sel_bias, "sel_bias", c.f32, E, dev),
-                                _arg(token_mask, "token_mask", c.mask, T, dev),
-                                _arg(topk_idx, "topk_idx", c.i32, T * k, dev),
-                                _arg(topk_w, "topk_w", c.f32, T * k, dev), _s(stream))
+    st = lib().moe_route_groups(
+        ctypes.byref(cfg), ctypes.byref(opts),
+        _arg(logits, "logits", c.of.get(opts.logits_dtype, ()), 0, dev, False), ld,
+        _arg(sel_bias, "sel_bias", c.f32, E, dev), _arg(token_mask, "token_mask", c.mask, T, dev),
+        _arg(topk_idx, "topk_idx", c.i32, T * k, dev), _arg(topk_w, "topk_w", c.f32, T * k, dev),
+        _s(stream))
     return _check(st, check)
 
 
 def moe_route_groups_backward(cfg, opts, logits, topk_idx, dw, dlogits, stream=None,
                               check=True) -> int:
     """dlogits [T, E] of <dw, topk_w> of moe_route_groups."""
-    T, k = cfg.T, cfg.top_k
-    ld, dld = _logits_ld(logits, cfg), _logits_ld(dlogits, cfg, "dlogits")
+    T, E, k = cfg.T, cfg.n_experts, cfg.top_k
+    ld, dld = _logits_ld(logits, T, E), _logits_ld(dlogits, T, E, "dlogits")
     if T == 0:
         logits = topk_idx = dw = dlogits = None
     c = _checks()
-    dev, own = c.device(), _of(c, opts)
-    st = lib().moe_route_groups_backward(ctypes.byref(cfg), ctypes.byref(opts),
-                                         _arg(logits, "logits", own, 0, dev, False), ld,
-                                         _arg(topk_idx, "topk_idx", c.i32, T * k, dev),
-                                         _arg(dw, "dw", c.f32, T * k, dev),
-                                         _arg(dlogits, "dlogits", own, 0, dev, False), dld,
-                                         _s(stream))
+    dev, own = c.device(), c.of.get(opts.logits_dtype, ())
+    st = lib().moe_route_groups_backward(
+        ctypes.byref(cfg), ctypes.byref(opts), _arg(logits, "logits", own, 0, dev, False), ld,
+        _arg(topk_idx, "topk_idx", c.i32, T * k, dev), _arg(dw, "dw", c.f32, T * k, dev),
+        _arg(dlogits, "dlogits", own, 0, dev, False), dld, _s(stream))
     return _check(st, check)
 
 
