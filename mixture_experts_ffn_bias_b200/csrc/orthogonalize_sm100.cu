@@ -180,6 +180,31 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
   if constexpr (CG == 2) tc_commit_pair(bar); else tc_commit(bar);
 }
 
+// Distributed shared memory: a variable's address in another CTA of the
+// cluster, stores to it, and barriers across it.
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void fence_cluster() {
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr)
+               : "memory");
+}
+// mbar_wait that also acquires what other CTAs of the cluster wrote.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity,
+                                                  volatile int* abort_flag) {
+  const bool ok = mbar_wait(bar, parity, abort_flag);
+  fence_cluster();
+  return ok;
+}
+
 __device__ __forceinline__ uint32_t half2_bits(__half2 v) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
@@ -372,10 +397,18 @@ struct NsMaps {
   CUtensorMap mir[2];   // gram, poly: the result in boxes of 64 rows x 64 columns
 };
 
-template <int MODE, int TERMS, int CG, int TN>
+// SPLIT > 1 (128 x 64 tiles, one per cluster): the CTAs of a cluster take a part
+// of the inner dimension each, hand the rows they do not finish to the CTA
+// that does through distributed shared memory, and finish 128 / SPLIT rows of
+// the tile.  With few tiles this shortens both the staging, which one SM's
+// share of L2 bandwidth bounds, and the epilogue.
+template <int MODE, int TERMS, int CG, int TN, int SPLIT>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
 ns_gemm_kernel(const __grid_constant__ NsMaps maps, const NsArgs args) {
   using C = Cfg<TERMS, CG, TN>;
+  static_assert(SPLIT == 1 || (CG == 1 && TN == 64), "split tiles");
+  constexpr int ROWS = 128 / SPLIT;               // rows of a tile this CTA finishes
+  constexpr int FINISHERS = EPI_WARPS / SPLIT;    // and its warps that do
   constexpr int STAGES = C::STAGES;
   constexpr int RATIO = C::TM / TN;
   constexpr bool BMN = MODE == MODE_APPLY || MODE == MODE_LAST;
@@ -395,13 +428,18 @@ ns_gemm_kernel(const __grid_constant__ NsMaps maps, const NsArgs args) {
   uint64_t* ready_bar = bars + 2 * STAGES + 4;    // a chunk buffer may be used
   uint64_t* done_bar = ready_bar + MAX_BUFS;      // and has been
   uint64_t* drain_bar = done_bar + MAX_BUFS;
+  uint64_t* parts_bar = drain_bar + 1;            // SPLIT: the other CTAs' sums are here
+  // their place, in planes a launch of one unmirrored tile a CTA does not use
+  float* parts = reinterpret_cast<float*>(sEpi + 2 * PLANE_BYTES);
   __shared__ uint32_t s_tmem_base;
   __shared__ int s_abort;
 
   pdl_trigger();   // the grid is resident at once: the next kernel may set up
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
-  const int unit = blockIdx.x / CG, units = gridDim.x / CG;
+  const int part = SPLIT > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int unit = blockIdx.x / (CG * SPLIT), units = gridDim.x / (CG * SPLIT);
+  const int k_first = args.kblocks * part / SPLIT, k_last = args.kblocks * (part + 1) / SPLIT;
   const long long total = static_cast<long long>(args.batch) * args.tiles;
   const int chunk_kb = TERMS == 3 ? CHUNK_KB : args.kblocks;
 
@@ -417,9 +455,10 @@ ns_gemm_kernel(const __grid_constant__ NsMaps maps, const NsArgs args) {
     }
     for (int i = 0; i < BUFS; ++i) {
       mbar_init(&ready_bar[i], 1);
-      mbar_init(&done_bar[i], EPI_WARPS);
+      mbar_init(&done_bar[i], FINISHERS);
     }
     mbar_init(drain_bar, 1);
+    if (SPLIT > 1) mbar_init(parts_bar, (SPLIT - 1) * FINISHERS);
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {
@@ -440,7 +479,7 @@ ns_gemm_kernel(const __grid_constant__ NsMaps maps, const NsArgs args) {
   pdl_wait();   // everything above touches no global memory
   tc_fence_before();
   __syncthreads();
-  if constexpr (CG == 2) cluster_sync_all();
+  if constexpr (CG * SPLIT > 1) cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem_base = s_tmem_base;
   volatile int* abort_flag = &s_abort;
@@ -458,7 +497,7 @@ ns_gemm_kernel(const __grid_constant__ NsMaps maps, const NsArgs args) {
                              ti, tj);
         const int arow = ti * C::TM + static_cast<int>(rank) * 128;
         const int bcol = tj * TN + static_cast<int>(rank) * (TN / CG);
-        for (int kb = 0; kb < args.kblocks; ++kb) {
+        for (int kb = k_first; kb < k_last; ++kb) {
           if (!mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag)) { ok = false; break; }
           if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], CG * C::STAGE_BYTES);
           uint8_t* sA = smem + stage * C::STAGE_BYTES;
@@ -499,8 +538,8 @@ ns_gemm_kernel(const __grid_constant__ NsMaps maps, const NsArgs args) {
       uint32_t phase = 0;
       bool ok = true, issued_any = false;
       for (long long t = unit; t < total && ok; t += units) {
-        for (int k0 = 0; k0 < args.kblocks && ok; k0 += chunk_kb, ++it) {
-          const int k1 = min(k0 + chunk_kb, args.kblocks);
+        for (int k0 = k_first; k0 < k_last && ok; k0 += chunk_kb, ++it) {
+          const int k1 = min(k0 + chunk_kb, k_last);
           const int acc = it & 1;
           if (!mbar_wait(&tempty_bar[acc], ((it >> 1) & 1) ^ 1u, abort_flag)) { ok = false; break; }
           tc_fence_after();
@@ -552,10 +591,11 @@ ns_gemm_kernel(const __grid_constant__ NsMaps maps, const NsArgs args) {
         if (MODE == MODE_GRAM) {
           mbar_arrive(&ready_bar[buf]);
         } else {
-          mbar_arrive_expect_tx(&ready_bar[buf], args.add_planes * PLANE_BYTES);
+          mbar_arrive_expect_tx(&ready_bar[buf], args.add_planes * ROWS * 128);
           for (int p = 0; p < args.add_planes; ++p)
-            tma_load_3d<1>(sEpi + buf * BUF_BYTES + p * PLANE_BYTES, &maps.add[p], &ready_bar[buf],
-                           tj * TN + in_c * 64, ti * C::TM + static_cast<int>(rank) * 128, b);
+            tma_load_3d<1>(sEpi + buf * BUF_BYTES + p * PLANE_BYTES + part * ROWS * 128,
+                           &maps.add[p], &ready_bar[buf], tj * TN + in_c * 64,
+                           ti * C::TM + static_cast<int>(rank) * 128 + part * ROWS, b);
         }
         if (++in_c == TN / 64) {
           in_c = 0;
@@ -575,11 +615,13 @@ ns_gemm_kernel(const __grid_constant__ NsMaps maps, const NsArgs args) {
         for (int c = 0; c < TN / 64; ++c, ++s) {
           const int buf = s % BUFS;
           if (!mbar_wait(&done_bar[buf], (s / BUFS) & 1, abort_flag)) { ok = false; break; }
-          const int row = ti * C::TM + static_cast<int>(rank) * 128, col = tj * TN + c * 64;
+          const int row = ti * C::TM + static_cast<int>(rank) * 128 + part * ROWS;
+          const int col = tj * TN + c * 64;
           const bool store = MODE != MODE_LAST && row < args.m && col < ncols;
           if (store) {
             for (int p = 0; p < args.out_planes; ++p)
-              tma_store_3d(&maps.out[p], sEpi + buf * BUF_BYTES + p * PLANE_BYTES, col, row, b);
+              tma_store_3d(&maps.out[p],
+                           sEpi + buf * BUF_BYTES + p * PLANE_BYTES + part * ROWS * 128, col, row, b);
             if (Chunks<MODE, TERMS, CG, TN>::STAGED && !args.full && tj >= RATIO * (ti + 1)) {
               for (int p = 0; p < args.out_planes; ++p)
                 for (int x = 0; x < 128 && row + x < args.m; x += 64)
@@ -644,7 +686,32 @@ ns_gemm_kernel(const __grid_constant__ NsMaps maps, const NsArgs args) {
       const int r = ti * C::TM + static_cast<int>(rank) * 128 + row;
       const bool mirror = !args.full && tj >= RATIO * (ti + 1);
       // one chunk: its buffer, the 32 sums, and the hand-over to the mover
-      auto chunk = [&](int c, const float (&f)[32]) {
+      auto chunk = [&](int c, float (&f)[32]) {
+        if constexpr (SPLIT > 1) {
+          const int owner = q * SPLIT / 4, rr = row % ROWS;   // who finishes these rows
+          if (owner != part) {
+            const uint32_t dst = map_rank(
+                smem_u32(parts + (part * 64 + half * 32) * ROWS + rr), owner);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) st_cluster_f32(dst + i * ROWS * 4, f[i]);
+            fence_cluster();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(map_rank(smem_u32(parts_bar), owner));
+            return true;
+          }
+          if (!__all_sync(0xffffffffu, mbar_wait_cluster(parts_bar, 0, abort_flag))) return false;
+          float own[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            own[i] = f[i];
+            f[i] = 0.f;
+          }
+#pragma unroll
+          for (int p = 0; p < SPLIT; ++p)      // in the order of the inner dimension
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              f[i] += p == part ? own[i] : parts[(p * 64 + half * 32 + i) * ROWS + rr];
+        }
         const int buf = s % BUFS;
         if (!wait(&ready_bar[buf], (s / BUFS) & 1)) return false;
         finish32<MODE, Chunks<MODE, TERMS, CG, TN>::STAGED>(args, f, sEpi + buf * BUF_BYTES, b, row, r, tj * TN + c * 64 + half * 32,
@@ -681,7 +748,7 @@ ns_gemm_kernel(const __grid_constant__ NsMaps maps, const NsArgs args) {
         for (int c = 0; c < TN / 64; ++c)
 #pragma unroll
           for (int i = 0; i < 32; ++i) sum[c][i] = 0.f;
-        for (int k0 = 0; k0 < args.kblocks; k0 += chunk_kb, ++it) {
+        for (int k0 = k_first; k0 < k_last; k0 += chunk_kb, ++it) {
           const int acc = it & 1;
           ok = wait(&tfull_bar[acc], (it >> 1) & 1);
           if (!ok) break;
@@ -708,7 +775,7 @@ ns_gemm_kernel(const __grid_constant__ NsMaps maps, const NsArgs args) {
 
   tc_fence_before();
   __syncthreads();
-  if constexpr (CG == 2) cluster_sync_all();   // neither CTA leaves the other early
+  if constexpr (CG * SPLIT > 1) cluster_sync_all();   // no CTA leaves the others early
   if (threadIdx.x == 0 && s_abort) atomicOr(args.status, kDevTimeout);
   if (warp == 1) {
     __syncwarp();
@@ -756,17 +823,9 @@ struct ClArgs {
   uint32_t* status;
 };
 
-__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
 __device__ __forceinline__ void st_cluster(uint32_t addr, const uint4& v) {
   asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};"
                ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 __device__ __forceinline__ void st_cluster_f64(uint32_t addr, double v) {
   asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
@@ -1393,10 +1452,10 @@ int num_sms() {
   return n;
 }
 
-template <int MODE, int TERMS, int CG, int TN>
+template <int MODE, int TERMS, int CG, int TN, int SPLIT = 1>
 cudaError_t launch_ns(const NsMaps& maps, NsArgs args, cudaStream_t stream) {
   using C = Cfg<TERMS, CG, TN>;
-  auto kern = ns_gemm_kernel<MODE, TERMS, CG, TN>;
+  auto kern = ns_gemm_kernel<MODE, TERMS, CG, TN, SPLIT>;
   static std::atomic<unsigned long long> attr_done{0};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -1412,7 +1471,7 @@ cudaError_t launch_ns(const NsMaps& maps, NsArgs args, cudaStream_t stream) {
   args.tn = ((SYM ? args.m : args.n) + TN - 1) / TN;
   const int max_units = num_sms() / CG;
   args.tiles = 0;
-  args.full = SYM && static_cast<long long>(args.batch) * args.tm * args.tn <= max_units;
+  args.full = SYM && (SPLIT > 1 || static_cast<long long>(args.batch) * args.tm * args.tn <= max_units);
   if (SYM && !args.full)
     for (int i = 0; i < args.tm; ++i) args.tiles += args.tn - C::TM / TN * i;
   else
@@ -1420,7 +1479,7 @@ cudaError_t launch_ns(const NsMaps& maps, NsArgs args, cudaStream_t stream) {
   const long long total = static_cast<long long>(args.batch) * args.tiles;
   const int units = static_cast<int>(total < max_units ? total : max_units);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(CG * units);
+  cfg.gridDim = dim3(CG * SPLIT * units);
   cfg.blockDim = dim3(NUM_THREADS);
   cfg.dynamicSmemBytes = C::SMEM_BYTES;
   cfg.stream = stream;
@@ -1428,7 +1487,7 @@ cudaError_t launch_ns(const NsMaps& maps, NsArgs args, cudaStream_t stream) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = CG;
+  attr[1].val.clusterDim.x = CG * SPLIT;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
@@ -1629,11 +1688,46 @@ TileShape choose_tiles(int batch, int m, int n, int kblocks) {
   return best;
 }
 
+// The added matrix and the result in chunks of 128, 64 and 32 rows (32: gram's
+// result only).
+struct ChunkMaps {
+  const CUtensorMap *add[3], *out[3];   // [rows][plane]
+};
+
 template <int MODE, int TERMS>
-cudaError_t launch_best(NsMaps& maps, const CUtensorMap (&b_op)[3][2], const NsArgs& args,
-                        cudaStream_t stream) {
+cudaError_t launch_best(NsMaps& maps, const CUtensorMap (&b_op)[3][2], const ChunkMaps& chunks,
+                        const NsArgs& args, cudaStream_t stream) {
   const TileShape t = choose_tiles<MODE, TERMS>(args.batch, args.m, args.n, args.kblocks);
-  for (int p = 0; p < 2; ++p) maps.b[p] = b_op[t][p];
+  // (an inner dimension of m that long has too many tiles, but for two CTAs
+  // with three terms)
+  constexpr bool FOUR = MODE == MODE_GRAM, TWO = MODE == MODE_GRAM || TERMS == 3;
+  int split = 1;
+  if (t == TILE_64) {
+    // Few tiles and a long inner dimension: split it over the SMs that would
+    // idle.  What the shorter loop saves against what a cluster and the
+    // exchange of the sums cost, in cycles (measured: [512, 512] fp32, 8
+    // k-blocks, gains nothing from four CTAs, [512, 2048] 206 -> 157 us).
+    constexpr bool SYM = MODE == MODE_GRAM || MODE == MODE_POLY;
+    const long long tiles = static_cast<long long>(args.batch) * ((args.m + 127) / 128) *
+                            (((SYM ? args.m : args.n) + 63) / 64);
+    const int sms = num_sms(), work = args.kblocks * (TERMS == 3 ? 1050 : 560);
+    int gain = 1500;
+    if (TWO && tiles * 2 <= sms && work / 2 - 3000 > gain) {
+      split = 2;
+      gain = work / 2 - 3000;
+    }
+    if (FOUR && tiles * 4 <= sms && work * 3 / 4 - 6000 > gain) split = 4;
+  }
+  const int rows = split == 4 ? 2 : split - 1;
+  for (int p = 0; p < 2; ++p) {
+    maps.b[p] = b_op[t][p];
+    maps.add[p] = chunks.add[rows][p];
+    maps.out[p] = chunks.out[rows][p];
+  }
+  if constexpr (FOUR)
+    if (split == 4) return launch_ns<MODE, TERMS, 1, 64, 4>(maps, args, stream);
+  if constexpr (TWO)
+    if (split == 2) return launch_ns<MODE, TERMS, 1, 64, 2>(maps, args, stream);
   return t == TILE_256   ? launch_ns<MODE, TERMS, 2, 256>(maps, args, stream)
          : t == TILE_128 ? launch_ns<MODE, TERMS, 2, 128>(maps, args, stream)
                          : launch_ns<MODE, TERMS, 1, 64>(maps, args, stream);
@@ -1651,11 +1745,11 @@ cudaError_t run_steps(const OrthoShape& s, void* out, void* ws, cudaStream_t str
   __half* al = TERMS == 3 ? reinterpret_cast<__half*>(w + L.al) : nullptr;
   __half* bh = reinterpret_cast<__half*>(w + L.bh);
   __half* bl = TERMS == 3 ? reinterpret_cast<__half*>(w + L.bl) : nullptr;
-  // Maps by box rows: 128 (A operand, chunks), 64 (mirrored tiles; X as the B
-  // operand of the apply product, MN-major).  The K-major B operand takes
+  // Maps by box rows: 128 (A operand, chunks), 64 and 32 (chunks of split tiles),
+  // 64 (mirrored tiles; X as the B operand of the apply product, MN-major).  The K-major B operand takes
   // 128 rows a CTA of the 256 x 256 tile, 64 of the others.
   CUtensorMap x128[2][2], x64[2][2];               // [buffer][plane]
-  CUtensorMap a128[2], a64[2], b128[2], b64[2];
+  CUtensorMap a128[2], a64[2], a32[2], b128[2], b64[2];
   for (int i = 0; i < 2; ++i)
     for (int p = 0; p < 2; ++p) {
       const void* base = w + (p ? L.xl[i] : L.xh[i]);
@@ -1663,12 +1757,16 @@ cudaError_t run_steps(const OrthoShape& s, void* out, void* ws, cudaStream_t str
           !make_map3(&x64[i][p], base, m, n, ldx, s.batch, bsx, 64))
         return cudaErrorInvalidValue;
     }
-  for (int p = 0; p < 2; ++p)
-    if (!make_map3(&a128[p], p && al ? al : ah, m, m, lda, s.batch, bsa, 128) ||
-        !make_map3(&a64[p], p && al ? al : ah, m, m, lda, s.batch, bsa, 64) ||
-        !make_map3(&b128[p], p && bl ? bl : bh, m, m, lda, s.batch, bsa, 128) ||
-        !make_map3(&b64[p], p && bl ? bl : bh, m, m, lda, s.batch, bsa, 64))
+  for (int p = 0; p < 2; ++p) {
+    const void* ap = p && al ? al : ah;
+    const void* bp = p && bl ? bl : bh;
+    if (!make_map3(&a128[p], ap, m, m, lda, s.batch, bsa, 128) ||
+        !make_map3(&a64[p], ap, m, m, lda, s.batch, bsa, 64) ||
+        !make_map3(&a32[p], ap, m, m, lda, s.batch, bsa, 32) ||
+        !make_map3(&b128[p], bp, m, m, lda, s.batch, bsa, 128) ||
+        !make_map3(&b64[p], bp, m, m, lda, s.batch, bsa, 64))
       return cudaErrorInvalidValue;
+  }
   static_assert(BK == 64, "boxes of X in the apply product");
   NsArgs base{};
   base.batch = s.batch;
@@ -1694,11 +1792,9 @@ cudaError_t run_steps(const OrthoShape& s, void* out, void* ws, cudaStream_t str
       maps.a[p] = x128[cur][p];
       b_op[TILE_256][p] = x128[cur][p];
       b_op[TILE_128][p] = b_op[TILE_64][p] = x64[cur][p];
-      maps.add[p] = a128[p];
-      maps.out[p] = a128[p];
       maps.mir[p] = a64[p];
     }
-    e = launch_best<MODE_GRAM, TERMS>(maps, b_op, g, stream);
+    e = launch_best<MODE_GRAM, TERMS>(maps, b_op, {{a128, a64, a32}, {a128, a64, a32}}, g, stream);
     if (e != cudaSuccess) return e;
     // B = b A + c A A
     NsArgs p = g;
@@ -1712,11 +1808,9 @@ cudaError_t run_steps(const OrthoShape& s, void* out, void* ws, cudaStream_t str
       maps.a[q] = a128[q];
       b_op[TILE_256][q] = a128[q];
       b_op[TILE_128][q] = b_op[TILE_64][q] = a64[q];
-      maps.add[q] = a128[q];
-      maps.out[q] = b128[q];
       maps.mir[q] = b64[q];
     }
-    e = launch_best<MODE_POLY, TERMS>(maps, b_op, p, stream);
+    e = launch_best<MODE_POLY, TERMS>(maps, b_op, {{a128, a64, a64}, {b128, b64, b64}}, p, stream);
     if (e != cudaSuccess) return e;
     // X = a X + B X; the last step of one-term products adds X's high plane
     // alone, so the step before it writes no other
@@ -1729,9 +1823,9 @@ cudaError_t run_steps(const OrthoShape& s, void* out, void* ws, cudaStream_t str
     for (int q = 0; q < 2; ++q) {
       maps.a[q] = b128[q];
       for (int t = 0; t < 3; ++t) b_op[t][q] = x64[cur][q];
-      maps.add[q] = x128[cur][q];
-      maps.out[q] = x128[cur ^ 1][q];
     }
+    const ChunkMaps chunks{{x128[cur], x64[cur], x64[cur]},
+                           {x128[cur ^ 1], x64[cur ^ 1], x64[cur ^ 1]}};
     if (last) {
       x.alpha *= s.scale / kScaleX;
       x.beta *= s.scale / kScaleX;
@@ -1740,9 +1834,9 @@ cudaError_t run_steps(const OrthoShape& s, void* out, void* ws, cudaStream_t str
       x.out_trans = trans;
       x.o_ld = s.out_ld;
       x.o_bs = s.out_bs;
-      e = launch_best<MODE_LAST, TERMS>(maps, b_op, x, stream);
+      e = launch_best<MODE_LAST, TERMS>(maps, b_op, chunks, x, stream);
     } else {
-      e = launch_best<MODE_APPLY, TERMS>(maps, b_op, x, stream);
+      e = launch_best<MODE_APPLY, TERMS>(maps, b_op, chunks, x, stream);
     }
     if (e != cudaSuccess) return e;
   }

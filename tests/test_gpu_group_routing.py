@@ -428,11 +428,13 @@ def _ref64(g, steps=5, coeffs=B.MUON_COEFFS, eps=1e-7):
 
 # every tile shape of every product, with and without mirrored tiles, ragged at
 # their edges; rows below 64 that do not fit one launch; widths from one to
-# sixteen CTAs of the one-launch kernel, four boxes a CTA, and both orders
+# sixteen CTAs of the one-launch kernel, four boxes a CTA, and both orders;
+# products split over two and four CTAs
 BATCHES = [(20, 400, 400), (9, 510, 510), (64, 250, 287), (64, 250, 250), (3, 900, 900),
            (40, 400, 805), (20, 700, 700), (9, 330, 331), (40, 130, 130), (6, 805, 400),
            (2, 40, 2500), (2, 2500, 40), (1, 128, 2048), (1, 1100, 100), (3, 100, 1500),
-           (150, 100, 250), (40, 70, 600), (5, 128, 129), (2, 129, 128), (1, 3, 2048)]
+           (150, 100, 250), (40, 70, 600), (5, 128, 129), (2, 129, 128), (1, 3, 2048),
+           (1, 512, 2048), (2, 256, 1024), (1, 130, 3000), (2, 3000, 140), (1, 513, 515)]
 
 
 @pytest.mark.parametrize("shape", BATCHES, ids=str)
