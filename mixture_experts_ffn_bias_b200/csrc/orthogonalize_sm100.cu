@@ -800,10 +800,11 @@ ns_gemm_kernel(const __grid_constant__ NsMaps maps, const NsArgs args) {
 //           to every CTA
 //   poly    B = b A + c A A, by every CTA for itself, in A's place
 //   apply   X = a X + B X on its own columns, in place
-// Three terms for both result types: with one tile a CTA the products cost
-// little.  What bounds it is latency: four block barriers and three cluster
-// barriers a step and their exchanges; 17 launches of the tiled kernel, 4 us
-// each with all their loads and stores, become one.
+// What bounds it is latency: the products of one tile (24 with three terms, 8
+// with one, at 90 cycles), their epilogues' conversions, four block barriers and
+// three cluster barriers a step with their exchanges ([128, 128] fp32 39.5 us;
+// [100, 192] 46.7 us, bf16 31.1); 17 launches of the tiled kernel, 4 us each with all their
+// loads and stores, become one.
 constexpr int CL_ROWS = 128;
 constexpr int CL_BOX = CL_ROWS * 128;            // bytes of a box's plane
 constexpr int CL_MAX_BOXES = 4;                  // of X per CTA
@@ -856,19 +857,25 @@ __device__ __forceinline__ void split8(const float* v, uint4& hi, uint4& lo) {
   }
 }
 
-// v = beta (hi + lo) + v over 8 elements of a row.
+// v = beta (hi + lo) + v over 8 elements of a row (PAIR; else of hi alone).
+template <bool PAIR>
 __device__ __forceinline__ void add8(const uint4& hi, const uint4& lo, float beta, float* v) {
   const __half2* h = reinterpret_cast<const __half2*>(&hi);
   const __half2* l = reinterpret_cast<const __half2*>(&lo);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(h[i]), g = __half22float2(l[i]);
-    v[2 * i] = fmaf(beta, f.x + g.x, v[2 * i]);
-    v[2 * i + 1] = fmaf(beta, f.y + g.y, v[2 * i + 1]);
+    float2 f = __half22float2(h[i]);
+    if (PAIR) {
+      const float2 g = __half22float2(l[i]);
+      f.x += g.x;
+      f.y += g.y;
+    }
+    v[2 * i] = fmaf(beta, f.x, v[2 * i]);
+    v[2 * i + 1] = fmaf(beta, f.y, v[2 * i + 1]);
   }
 }
 
-template <typename T, bool TRANS, int CL>
+template <typename T, bool TRANS, int CL, int TERMS>
 __global__ void __launch_bounds__(CL_THREADS, 1)
 ns_cluster_kernel(const ClArgs args) {
   extern __shared__ uint8_t smem_raw[];
@@ -877,9 +884,10 @@ ns_cluster_kernel(const ClArgs args) {
   const int nbx = args.nbx;
   uint8_t* xh = smem;                              // X: nbx boxes of each plane
   uint8_t* xl = xh + nbx * CL_BOX;
-  uint8_t* ah = xl + nbx * CL_BOX;                 // A, then B: two boxes of each
-  uint8_t* al = ah + 2 * CL_BOX;
-  float* recv = reinterpret_cast<float*>(args.recv_apart ? al + 2 * CL_BOX : ah);
+  uint8_t* ah = xl + nbx * CL_BOX;                 // A, then B: two boxes of each plane
+  uint8_t* al = ah + 2 * CL_BOX;                   // (TERMS 3)
+  float* recv =
+      reinterpret_cast<float*>(args.recv_apart ? ah + (TERMS == 3 ? 4 : 2) * CL_BOX : ah);
   __shared__ uint64_t s_bar;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
@@ -1013,7 +1021,7 @@ ns_cluster_kernel(const ClArgs args) {
     if (tid == 0) {
       tc_fence_after();
       uint32_t first = 0;
-      for (int term = 0; term < 3; ++term)   // hi lo, lo hi, hi hi
+      for (int term = 3 - TERMS; term < 3; ++term)   // hi lo, lo hi, hi hi
         for (int bx = 0; bx < nbx; ++bx) {
           const uint32_t pa = smem_u32(term == 1 ? xl : xh) + bx * CL_BOX;
           const uint32_t pb = smem_u32(term == 0 ? xl : xh) + bx * CL_BOX;
@@ -1037,7 +1045,7 @@ ns_cluster_kernel(const ClArgs args) {
           uint4 hi, lo;
           split8(f + 8 * i, hi, lo);
           *piece(sq_h, row, sq_piece + i) = hi;
-          *piece(sq_l, row, sq_piece + i) = lo;
+          if (TERMS == 3) *piece(sq_l, row, sq_piece + i) = lo;
         }
       }
     } else {
@@ -1095,7 +1103,7 @@ ns_cluster_kernel(const ClArgs args) {
         for (uint32_t i = 0; i < CL; ++i) {
           const uint32_t t = (rank + i) % CL;      // not all to one CTA at a time
           st_cluster(map_rank(ph, t), hi);
-          st_cluster(map_rank(pl, t), lo);
+          if (TERMS == 3) st_cluster(map_rank(pl, t), lo);
         }
       }
       fence_proxy_async_all();
@@ -1108,7 +1116,7 @@ ns_cluster_kernel(const ClArgs args) {
     if (tid == 0) {
       tc_fence_after();
       uint32_t first = 0;
-      for (int term = 0; term < 3; ++term)
+      for (int term = 3 - TERMS; term < 3; ++term)
         for (int k = 0; k < mp; k += 16) {
           const uint32_t off = (k >> 6) * CL_BOX + (k & 63) * 2;
           tc_mma_f16(d_sq, smem_desc_sw128(smem_u32(term == 1 ? al : ah) + off),
@@ -1125,11 +1133,11 @@ ns_cluster_kernel(const ClArgs args) {
       for (int i = 0; i < 4; ++i) {
         uint4* ph = piece(sq_h, row, sq_piece + i);
         uint4* pl = piece(sq_l, row, sq_piece + i);
-        add8(*ph, *pl, args.b, f + 8 * i);
+        add8<TERMS == 3>(*ph, TERMS == 3 ? *pl : *ph, args.b, f + 8 * i);
         uint4 hi, lo;
         split8(f + 8 * i, hi, lo);
         *ph = hi;
-        *pl = lo;
+        if (TERMS == 3) *pl = lo;
       }
     }
     fence_proxy_async_all();
@@ -1139,7 +1147,7 @@ ns_cluster_kernel(const ClArgs args) {
     if (tid == 0) {
       tc_fence_after();
       uint32_t first = 0;
-      for (int term = 0; term < 3; ++term)
+      for (int term = 3 - TERMS; term < 3; ++term)
         for (int k = 0; k < mp; k += 16) {
           const uint32_t off = (k >> 6) * CL_BOX + (k & 63) * 2;
           tc_mma_f16(d_x, smem_desc_sw128(smem_u32(term == 1 ? al : ah) + off),
@@ -1163,7 +1171,10 @@ ns_cluster_kernel(const ClArgs args) {
         for (int i = 0; i < 4; ++i) {
           uint4* ph = piece(xh + bx * CL_BOX, row, half * 4 + i);
           uint4* pl = piece(xl + bx * CL_BOX, row, half * 4 + i);
-          add8(*ph, *pl, xs * args.a, f + 8 * i);
+          if (TERMS == 3 || !last)   // one term: the last step adds the high plane alone
+            add8<true>(*ph, *pl, xs * args.a, f + 8 * i);
+          else
+            add8<false>(*ph, *ph, xs * args.a, f + 8 * i);
           if (!last) {
             uint4 hi, lo;
             split8(f + 8 * i, hi, lo);
@@ -1534,24 +1545,27 @@ OrthoLayout ortho_layout(const OrthoShape& s) {
   return L;
 }
 
-// CTAs per cluster of the one-launch kernel, 0 where it does not apply.
-// Columns go to as many CTAs as keep two boxes each while every matrix has
-// its cluster at once; else four boxes each.  16 CTAs, more than a cluster
-// is sure to get, only for single matrices wider than 8 of them take so
-// ([128, 2048] fp32: 85 us on 8 CTAs, 72 us on 16).
+// CTAs per cluster of the one-launch kernel, 0 where it does not apply.  Up to
+// four boxes stay in one CTA, which needs no exchange ([100, 192] bf16 31.1 us,
+// on two CTAs 38.8; fp32 of 256 columns 54.3, on four 51.2).  Above, two boxes a
+// CTA while every matrix has its cluster at once ([100, 512] bf16 41 us on four
+// CTAs, 51 on two; [100, 1024] 45 on eight, 52 on four), else four: the 16th
+// cluster of eight waits for another to end (16 of [100, 1024] bf16: 91 us on
+// eight CTAs each, 53 on four).  16 CTAs, more than a cluster is sure to get,
+// only for single matrices wider than 8 of them take so ([128, 2048] fp32: 85 us
+// on 8 CTAs, 72 us on 16).
 int cluster_size(int batch, int m, int n) {
   if (m > CL_ROWS || n > 8 * CL_MAX_BOXES * 64) return 0;
   const int boxes = (n + 63) / 64;
-  int wide = 1, narrow = 1;   // by four and by two boxes a CTA
-  while (wide * CL_MAX_BOXES < boxes) wide *= 2;
-  while (narrow * 2 < boxes && narrow < 16) narrow *= 2;
-  if (narrow == 16) return batch <= 2 ? 16 : 8;
-  return static_cast<long long>(batch) * narrow <= 128 ? narrow : wide;
+  if (boxes <= CL_MAX_BOXES) return 1;
+  if (boxes <= 8) return batch <= 32 ? 4 : 2;
+  if (boxes <= 16) return batch <= 12 ? 8 : 4;
+  return batch <= 2 ? 16 : 8;
 }
 
-template <typename T, bool TRANS, int CL>
+template <typename T, bool TRANS, int CL, int TERMS>
 cudaError_t launch_cluster(const ClArgs& args, int smem, cudaStream_t stream) {
-  auto kern = ns_cluster_kernel<T, TRANS, CL>;
+  auto kern = ns_cluster_kernel<T, TRANS, CL, TERMS>;
   static std::atomic<unsigned long long> attr_done{0};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -1597,7 +1611,7 @@ cudaError_t launch_cluster(const ClArgs& args, int smem, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, kern, args);
 }
 
-template <typename T>
+template <typename T, int TERMS>
 cudaError_t run_cluster(const OrthoShape& s, int cl, const void* g, void* out, void* ws,
                         cudaStream_t stream) {
   const bool trans = s.rows > s.cols;
@@ -1620,28 +1634,30 @@ cudaError_t run_cluster(const OrthoShape& s, int cl, const void* g, void* out, v
   a.o_ld = s.out_ld;
   a.o_bs = s.out_bs;
   a.status = static_cast<uint32_t*>(ws);
-  // X's and A's planes; the received rows apart while that fits, else in A's
-  // place (of the same size)
+  // X's and A's planes; the received rows apart while that fits, else in the
+  // place of A's two planes, which is as large
   static_assert(CL_RECV_BYTES == 4 * CL_BOX, "A's planes");
-  int smem = (2 * a.nbx + 4) * CL_BOX + 1024;
+  static_assert((2 * CL_MAX_BOXES + 2) * CL_BOX + 1024 + CL_RECV_BYTES <= 232448 - 512,
+                "one term: always apart");
+  int smem = (2 * a.nbx + (TERMS == 3 ? 4 : 2)) * CL_BOX + 1024;
   if (cl > 1) {
     a.recv_apart = smem + CL_RECV_BYTES <= 232448 - 512;
     if (a.recv_apart) smem += CL_RECV_BYTES;
   }
   if (cl == 16) {
-    const cudaError_t e = trans ? launch_cluster<T, true, 16>(a, smem, stream)
-                                : launch_cluster<T, false, 16>(a, smem, stream);
-    return e == cudaErrorInvalidConfiguration ? run_cluster<T>(s, 8, g, out, ws, stream) : e;
+    const cudaError_t e = trans ? launch_cluster<T, true, 16, TERMS>(a, smem, stream)
+                                : launch_cluster<T, false, 16, TERMS>(a, smem, stream);
+    return e == cudaErrorInvalidConfiguration ? run_cluster<T, TERMS>(s, 8, g, out, ws, stream) : e;
   }
   auto go = [&](auto one, auto two, auto four, auto eight) {
     return cl == 1 ? one(a, smem, stream)
                    : cl == 2 ? two(a, smem, stream)
                              : cl == 4 ? four(a, smem, stream) : eight(a, smem, stream);
   };
-  return trans ? go(launch_cluster<T, true, 1>, launch_cluster<T, true, 2>,
-                    launch_cluster<T, true, 4>, launch_cluster<T, true, 8>)
-               : go(launch_cluster<T, false, 1>, launch_cluster<T, false, 2>,
-                    launch_cluster<T, false, 4>, launch_cluster<T, false, 8>);
+  return trans ? go(launch_cluster<T, true, 1, TERMS>, launch_cluster<T, true, 2, TERMS>,
+                    launch_cluster<T, true, 4, TERMS>, launch_cluster<T, true, 8, TERMS>)
+               : go(launch_cluster<T, false, 1, TERMS>, launch_cluster<T, false, 2, TERMS>,
+                    launch_cluster<T, false, 4, TERMS>, launch_cluster<T, false, 8, TERMS>);
 }
 
 // Tile shapes of the tiled kernel: 256 x 256 and 256 x 128 on CTA pairs, 128 x 64
@@ -1885,8 +1901,11 @@ cudaError_t orthogonalize(const OrthoShape& s, const void* g, void* out, void* w
   const int m = s.rows < s.cols ? s.rows : s.cols, n = s.rows < s.cols ? s.cols : s.rows;
   const int cl = cluster_size(s.batch, m, n);
   if (cl > 0)
-    return s.in_bf16 ? run_cluster<__nv_bfloat16>(s, cl, g, out, ws, stream)
-                     : run_cluster<float>(s, cl, g, out, ws, stream);
+    return three_terms(s)
+               ? (s.in_bf16 ? run_cluster<__nv_bfloat16, 3>(s, cl, g, out, ws, stream)
+                            : run_cluster<float, 3>(s, cl, g, out, ws, stream))
+               : (s.in_bf16 ? run_cluster<__nv_bfloat16, 1>(s, cl, g, out, ws, stream)
+                            : run_cluster<float, 1>(s, cl, g, out, ws, stream));
   cudaError_t e = s.in_bf16 ? run_init(s, static_cast<const __nv_bfloat16*>(g), ws, stream)
                             : run_init(s, static_cast<const float*>(g), ws, stream);
   if (e != cudaSuccess) return e;

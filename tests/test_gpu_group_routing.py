@@ -434,7 +434,9 @@ BATCHES = [(20, 400, 400), (9, 510, 510), (64, 250, 287), (64, 250, 250), (3, 90
            (40, 400, 805), (20, 700, 700), (9, 330, 331), (40, 130, 130), (6, 805, 400),
            (2, 40, 2500), (2, 2500, 40), (1, 128, 2048), (1, 1100, 100), (3, 100, 1500),
            (150, 100, 250), (40, 70, 600), (5, 128, 129), (2, 129, 128), (1, 3, 2048),
-           (1, 512, 2048), (2, 256, 1024), (1, 130, 3000), (2, 3000, 140), (1, 513, 515)]
+           (1, 512, 2048), (2, 256, 1024), (1, 130, 3000), (2, 3000, 140), (1, 513, 515),
+           (40, 70, 500), (33, 260, 90), (4, 66, 400), (13, 1000, 90), (12, 90, 1000),
+           (13, 1025, 65), (70, 64, 256)]
 
 
 @pytest.mark.parametrize("shape", BATCHES, ids=str)
@@ -469,11 +471,12 @@ def test_orthogonalize_steps_and_coefficients(dout, steps, coeffs, scale):
 
 
 @pytest.mark.parametrize("dout", [torch.float32, torch.bfloat16])
-def test_orthogonalize_low_rank(dout):
+@pytest.mark.parametrize("rows,cols", [(200, 300), (100, 180), (600, 66)])
+def test_orthogonalize_low_rank(dout, rows, cols):
     """Few strong directions over noise 1e-4 of them, which grows by 3.44 a
     step: bf16 results keep the iterate to 22 bits for this."""
     rng = np.random.default_rng(3)
-    a = rng.standard_normal((2, 200, 12)) @ rng.standard_normal((2, 12, 300))
+    a = rng.standard_normal((2, rows, 12)) @ rng.standard_normal((2, 12, cols))
     g = torch.from_numpy((a + 1e-4 * rng.standard_normal(a.shape)).astype(np.float32)).cuda()
     out, _ = _ortho(g, dout)
     # fp32: the noise directions are 1e-4 of the operands' 2^-22, so 1e-3 of
