@@ -353,10 +353,15 @@ class _Types:
         self.mask = (torch.uint8, torch.bool)
         self.of = {DTYPE_F32: (torch.float32,), DTYPE_BF16: (torch.bfloat16,)}
         self._ready, self._device = torch.cuda.is_initialized, torch._C._cuda_getDevice
+        self._raw = torch._C._cuda_getCurrentRawStream
 
-    def device(self) -> int:
-        """The current CUDA device (-2, like no tensor's, before CUDA is in use)."""
-        return self._device() if self._ready() else -2
+    def here(self, stream):
+        """The current CUDA device (-2, like no tensor's, before CUDA is in use)
+        and the stream to use on it."""
+        if not self._ready():
+            return -2, _s(stream)
+        dev = self._device()
+        return dev, self._raw(dev) if stream is None else _s(stream)
 
 
 _types = None
@@ -410,13 +415,13 @@ def moe_route_groups(cfg, opts, logits, sel_bias, token_mask, topk_idx, topk_w, 
     if T == 0:
         logits = sel_bias = token_mask = topk_idx = topk_w = None
     c = _checks()
-    dev = c.device()
+    dev, s = c.here(stream)
     st = lib().moe_route_groups(
         ctypes.byref(cfg), ctypes.byref(opts),
         _arg(logits, "logits", c.of.get(opts.logits_dtype, ()), 0, dev, False), ld,
         _arg(sel_bias, "sel_bias", c.f32, E, dev), _arg(token_mask, "token_mask", c.mask, T, dev),
         _arg(topk_idx, "topk_idx", c.i32, T * k, dev), _arg(topk_w, "topk_w", c.f32, T * k, dev),
-        _s(stream))
+        s)
     return _check(st, check)
 
 
@@ -428,11 +433,11 @@ def moe_route_groups_backward(cfg, opts, logits, topk_idx, dw, dlogits, stream=N
     if T == 0:
         logits = topk_idx = dw = dlogits = None
     c = _checks()
-    dev, own = c.device(), c.of.get(opts.logits_dtype, ())
+    (dev, s), own = c.here(stream), c.of.get(opts.logits_dtype, ())
     st = lib().moe_route_groups_backward(
         ctypes.byref(cfg), ctypes.byref(opts), _arg(logits, "logits", own, 0, dev, False), ld,
         _arg(topk_idx, "topk_idx", c.i32, T * k, dev), _arg(dw, "dw", c.f32, T * k, dev),
-        _arg(dlogits, "dlogits", own, 0, dev, False), dld, _s(stream))
+        _arg(dlogits, "dlogits", own, 0, dev, False), dld, s)
     return _check(st, check)
 
 
@@ -442,12 +447,12 @@ def moe_forward_grouped(cfg, groups, x, w_router, sel_bias, logit_offset, token_
     """moe_forward routed by moe_route_groups (groups: MoEGroupOpts)."""
     w = expert_weights(weights)
     c = _checks()
-    mask = _arg(token_mask, "token_mask", c.mask, cfg.T, c.device())
+    dev, s = c.here(stream)
+    mask = _arg(token_mask, "token_mask", c.mask, cfg.T, dev)
     st = lib().moe_forward_grouped(ctypes.byref(cfg), ctypes.byref(groups), _p(x), _p(w_router),
                                    _p(sel_bias), _p(logit_offset), mask,
                                    ctypes.byref(w), _p(out), _p(topk_idx), _p(topk_w),
-                                   _p(counts), _p(ws), _nbytes(ws) if ws is not None else 0,
-                                   _s(stream))
+                                   _p(counts), _p(ws), _nbytes(ws) if ws is not None else 0, s)
     return _check(st, check)
 
 
@@ -500,11 +505,13 @@ def moe_orthogonalize(cfg, g, out, ws, stream=None, check=True) -> int:
     if cfg.batch == 0:
         g = out = None
     t = _checks()
-    dev = t.device()
+    dev, s = t.here(stream)
+    if getattr(ws, "dtype", None) is not None and ws.get_device() != dev:
+        raise MoEError(MOE_ERR_INVALID, f"ws: expected on the current CUDA device, got {ws.device}")
     st = lib().moe_orthogonalize(ctypes.byref(c),
                                  _arg(g, "g", t.of.get(cfg.dtype_in, ()), 0, dev, False),
                                  _arg(out, "out", t.of.get(cfg.dtype_out, ()), 0, dev, False),
-                                 _p(ws), _nbytes(ws) if ws is not None else 0, _s(stream))
+                                 _p(ws), _nbytes(ws) if ws is not None else 0, s)
     return _check(st, check)
 
 
