@@ -786,15 +786,20 @@ route_kernel(const RouteShape a, const L* __restrict__ logits, const float* __re
 //   1  (softmax) the warp reads one token's row after another and leaves the
 //      exponentials in shared memory
 //   2  lane `sub` of a token takes the pairs sub, sub + 8, ..
-//   3  the rows without the chosen experts' own part (sigmoid: zeros), then
-//      the chosen elements over them
+//      and leaves their elements in the row in shared memory
+//   3  the rows: those elements, the exponentials' multiples (sigmoid: zeros)
+//      elsewhere, each row written once
 // Memory bound: a row is read (softmax) and written once.
-template <typename L, bool VEC>
+// NP: pairs of a lane, rounded up to a power of two.
+// No early trigger: blocks of the next launch that wait beside this one's leave
+// its blocks uneven over the SMs ([16384, 128] softmax: 6.9 us with, 6.15
+// without).  [131072, 256] fp32 sigmoid: 33 to 35 us, 134 MB written and a
+// sector read for each pair, 0.75 of the copy bandwidth.
+template <typename L, int NP, bool VEC>
 __global__ void __launch_bounds__(32 * kRouteWarps)
 route_bwd_kernel(const RouteShape a, const L* __restrict__ logits,
                  const int32_t* __restrict__ topk_idx, const float* __restrict__ dw,
                  L* __restrict__ dlogits, long long dld) {
-  pdl_trigger();
   pdl_wait();
   extern __shared__ __align__(16) float smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -853,13 +858,13 @@ route_bwd_kernel(const RouteShape a, const L* __restrict__ logits,
   __syncwarp();
   // -------------------------------------------------------------- 2 pairs
   const int t = t0 + tok;
-  int e[kMaxK / 8];
-  float d[kMaxK / 8], sj[kMaxK / 8], v[kMaxK / 8];
+  int e[NP];
+  float d[NP], sj[NP], v[NP];
   double D = 0.0, Q = 0.0;
   bool twice = false;
   bool some = false;
 #pragma unroll
-  for (int i = 0; i < kMaxK / 8; ++i) {
+  for (int i = 0; i < NP; ++i) {
     const int j = sub + 8 * i;
     e[i] = -1;
     d[i] = 0.f;
@@ -897,9 +902,9 @@ route_bwd_kernel(const RouteShape a, const L* __restrict__ logits,
     f = static_cast<double>(a.scale) / (D * D);
   }
   double dot = 0.0;
-  float ds[kMaxK / 8];
+  float ds[NP];
 #pragma unroll
-  for (int i = 0; i < kMaxK / 8; ++i) {
+  for (int i = 0; i < NP; ++i) {
     ds[i] = 0.f;
     if (8 * i >= a.k || e[i] < 0) continue;
     q = a.norm ? f * (static_cast<double>(d[i]) * D - Q) : f * static_cast<double>(d[i]);
@@ -912,25 +917,29 @@ route_bwd_kernel(const RouteShape a, const L* __restrict__ logits,
   }
   if (__any_sync(kFull, twice)) {
     // an expert listed twice: the sum of its pairs, in pair order, at each
-    float sum[kMaxK / 8];
+    float sum[NP];
 #pragma unroll
-    for (int i = 0; i < kMaxK / 8; ++i) sum[i] = 0.f;
+    for (int i = 0; i < NP; ++i) sum[i] = 0.f;
 #pragma unroll
-    for (int ih = 0; ih < kMaxK / 8; ++ih) {
+    for (int ih = 0; ih < NP; ++ih) {
       if (8 * ih >= a.k) continue;
       for (int hl = 0; hl < 8; ++hl) {
         const int eh = __shfl_sync(kFull, e[ih], (tok << 3) | hl);
         const float dh = __shfl_sync(kFull, ds[ih], (tok << 3) | hl);
 #pragma unroll
-        for (int i = 0; i < kMaxK / 8; ++i)
+        for (int i = 0; i < NP; ++i)
           if (eh == e[i]) sum[i] += dh;
       }
     }
 #pragma unroll
-    for (int i = 0; i < kMaxK / 8; ++i) ds[i] = sum[i];
+    for (int i = 0; i < NP; ++i) ds[i] = sum[i];
   }
   const unsigned with = __ballot_sync(kFull, some);
   const float fdot = soft ? static_cast<float>(dot) : 0.f;
+#pragma unroll
+  for (int i = 0; i < NP; ++i)
+    if (e[i] >= 0) rows[tok * ROW + e[i]] = v[i] * (ds[i] - fdot);
+  __syncwarp();
   // --------------------------------------------------------------- 3 rows
   const float neg = -fdot * row_inv;
 #pragma unroll
@@ -947,9 +956,13 @@ route_bwd_kernel(const RouteShape a, const L* __restrict__ logits,
         const int x = 4 * lane + 128 * i;
         if (x >= a.E) break;
         float4 g = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (dense) {
-          g = *reinterpret_cast<const float4*>(row + x);
-          g = make_float4(g.x * c, g.y * c, g.z * c, g.w * c);
+        const unsigned own = seen[8 * r + (x >> 5)] >> (x & 31);   // chosen ones: as they are
+        if (dense || (own & 15u)) {
+          const float4 q = *reinterpret_cast<const float4*>(row + x);
+          g.x = own & 1u ? q.x : dense ? q.x * c : 0.f;
+          g.y = own & 2u ? q.y : dense ? q.y * c : 0.f;
+          g.z = own & 4u ? q.z : dense ? q.z * c : 0.f;
+          g.w = own & 8u ? q.w : dense ? q.w * c : 0.f;
         }
         if constexpr (sizeof(L) == 2) {
           const __nv_bfloat162 h0 = __floats2bfloat162_rn(g.x, g.y);
@@ -963,18 +976,11 @@ route_bwd_kernel(const RouteShape a, const L* __restrict__ logits,
       }
     } else {
       for (int x = lane; x < a.E; x += 32) {
-        const float g = dense ? row[x] * c : 0.f;
+        const bool own = (seen[8 * r + (x >> 5)] >> lane) & 1u;
+        const float g = own ? row[x] : dense ? row[x] * c : 0.f;
         if constexpr (sizeof(L) == 2) out[x] = __float2bfloat16_rn(g); else out[x] = g;
       }
     }
-  }
-  __syncwarp();                                    // the rows before their chosen elements
-#pragma unroll
-  for (int i = 0; i < kMaxK / 8; ++i) {
-    if (8 * i >= a.k || e[i] < 0) continue;
-    L* out = dlogits + static_cast<size_t>(t) * dld + e[i];
-    const float g = v[i] * (ds[i] - fdot);
-    if constexpr (sizeof(L) == 2) *out = __float2bfloat16_rn(g); else *out = g;
   }
 }
 
@@ -1026,9 +1032,13 @@ cudaError_t route_bwd_launch(const RouteShape& a, const L* logits, const int32_t
   const bool vec = a.E % 4 == 0 && a.ld % 4 == 0 && dld % 4 == 0 &&
                    (reinterpret_cast<uintptr_t>(logits) & align) == 0 &&
                    (reinterpret_cast<uintptr_t>(dlogits) & align) == 0;
-  auto kern = vec ? route_bwd_kernel<L, true> : route_bwd_kernel<L, false>;
-  return launch_pdl(kern, dim3(grid), dim3(32 * warps), smem, stream, a, logits, topk_idx, dw,
-                    dlogits, dld);
+  auto go = [&](auto kern) {
+    return launch_pdl(kern, dim3(grid), dim3(32 * warps), smem, stream, a, logits, topk_idx, dw,
+                      dlogits, dld);
+  };
+  if (a.k <= 8) return vec ? go(route_bwd_kernel<L, 1, true>) : go(route_bwd_kernel<L, 1, false>);
+  if (a.k <= 16) return vec ? go(route_bwd_kernel<L, 2, true>) : go(route_bwd_kernel<L, 2, false>);
+  return vec ? go(route_bwd_kernel<L, 4, true>) : go(route_bwd_kernel<L, 4, false>);
 }
 
 }  // namespace
