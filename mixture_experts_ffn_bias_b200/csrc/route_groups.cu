@@ -17,13 +17,17 @@
 // tail of every launch); a token with values fp32 cannot rank is decided
 // again as a whole in fp64.
 //
-// Bound by memory for many tokens (the logits are read once), by the
-// selection's instructions close behind: 4 tokens per warp, 8 lanes each, so
-// that the cross-lane steps of the top-k serve four tokens at a time.
+// Bound by the selection's instructions for many tokens: 4 tokens per warp, 8
+// lanes each, so that the cross-lane steps of the top-k serve four tokens at a
+// time.  [131072, 256] fp32, 8 groups of which 4, top-8: 74 us, 1.8 TB/s of
+// logits, about 1950 instructions a warp (of 82 us with blocks of four warps,
+// the rounds of the top-k took 25, the groups 18, the keys 12, the margins 1).
+// [16384, 128]: 9.7 us.  One token: 4 us, of which the launch is half.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "kernels.h"
 #include "launch.cuh"
@@ -347,8 +351,9 @@ constexpr int kPickRow = kMaxK + 2 + kMorePicks;
 //      after the rounds
 //   4  weights
 // NB: blocks of 4 experts of a lane in step 3, rounded up to a power of two.
-template <typename L, int NB, bool VEC>
-__global__ void __launch_bounds__(32 * kRouteWarps, 7)
+// WARPS: at most, of a block.
+template <typename L, int NB, bool VEC, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, WARPS == kRouteWarps ? 7 : 4)
 route_kernel(const RouteShape a, const L* __restrict__ logits, const float* __restrict__ bias,
              const uint8_t* __restrict__ mask, int32_t* __restrict__ topk_idx,
              float* __restrict__ topk_w) {
@@ -1002,23 +1007,38 @@ template <typename L>
 cudaError_t route_launch(const RouteShape& a, const L* logits, const float* bias,
                          const uint8_t* mask, int32_t* topk_idx, float* topk_w,
                          cudaStream_t stream) {
-  // one warp per block until there are enough tokens for four on every SM
-  const int warps = a.T <= 148 * 16 ? 1 : kRouteWarps;
+  const int per = a.per;
+  const int total = a.topk_group < a.groups && per % 4 == 0 ? a.topk_group * per : a.E;
+  // One warp per block until there are enough tokens for four on every SM.
+  // Eight, which share the bias and keep 32 warps on an SM instead of 28, for
+  // three rounds of tokens and more ([131072, 256] 80.3 us with four, 74.1 with
+  // eight; below, the coarser last round costs more: [16384, 128] 9.6 and 10.2),
+  // but for more than 4 blocks a lane, whose registers that leaves too few
+  // ([131072, 160] without groups 75.9 and 78.5).
+  const int warps = a.T <= 148 * 16 ? 1
+                    : a.T <= 3 * 148 * 28 * 4 || total > 128 ? kRouteWarps : 2 * kRouteWarps;
   const unsigned grid = static_cast<unsigned>((a.T + 4 * warps - 1) / (4 * warps));
   const size_t row = 36 * ((a.E + 31) / 32);   // floats of a token's keys, and of the bias
   const size_t smem = (row + warps * (4 * row + 8 * kPickRow)) * sizeof(float);
+  static_assert((288 + 2 * kRouteWarps * (4 * 288 + 8 * kPickRow)) * sizeof(float) <= 49152,
+                "shared memory of a block without asking");
   const bool vec = a.E % 4 == 0 && a.ld % 4 == 0 &&
                    (reinterpret_cast<uintptr_t>(logits) & (4 * sizeof(L) - 1)) == 0;
-  const int per = a.per;
-  const int total = a.topk_group < a.groups && per % 4 == 0 ? a.topk_group * per : a.E;
   auto go = [&](auto kern) {
     return launch_pdl(kern, dim3(grid), dim3(32 * warps), smem, stream, a, logits, bias, mask,
                       topk_idx, topk_w);
   };
-  if (total <= 32) return vec ? go(route_kernel<L, 1, true>) : go(route_kernel<L, 1, false>);
-  if (total <= 64) return vec ? go(route_kernel<L, 2, true>) : go(route_kernel<L, 2, false>);
-  if (total <= 128) return vec ? go(route_kernel<L, 4, true>) : go(route_kernel<L, 4, false>);
-  return vec ? go(route_kernel<L, 8, true>) : go(route_kernel<L, 8, false>);
+  constexpr int W = kRouteWarps;
+  auto best = [&](auto nb) {
+    constexpr int NB = decltype(nb)::value;
+    if (warps > W)
+      return vec ? go(route_kernel<L, NB, true, 2 * W>) : go(route_kernel<L, NB, false, 2 * W>);
+    return vec ? go(route_kernel<L, NB, true, W>) : go(route_kernel<L, NB, false, W>);
+  };
+  if (total <= 32) return best(std::integral_constant<int, 1>{});
+  if (total <= 64) return best(std::integral_constant<int, 2>{});
+  if (total <= 128) return best(std::integral_constant<int, 4>{});
+  return vec ? go(route_kernel<L, 8, true, W>) : go(route_kernel<L, 8, false, W>);
 }
 
 template <typename L>

@@ -256,6 +256,24 @@ def test_routing_many_tokens_match_the_fp64_selection():
         assert torch.all((w.double() - rw).abs() <= W_RTOL * rw)
 
 
+@pytest.mark.parametrize("E,k,groups,topk_group,pad", [(96, 6, 6, 2, 0), (63, 5, 1, 1, 1),
+                                                       (128, 8, 8, 4, 0), (250, 9, 25, 7, 3)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_routing_a_long_batch_as_its_pieces(E, k, groups, topk_group, pad, dtype):
+    """Large calls use larger blocks: tokens choose what they choose in small
+    calls (which are checked against the oracle)."""
+    T = 50003
+    l = _logits(T, E, E + T, dtype, pad)
+    mask = (torch.rand(T, device="cuda") > 0.1).to(torch.uint8)
+    bias = torch.linspace(-0.05, 0.05, E, device="cuda")
+    kw = dict(bias=bias, groups=groups, topk_group=topk_group, scale=1.5)
+    _, _, idx, w = _route(l, k, mask=mask, **kw)
+    for i in range(0, T, 2000):
+        _, _, pi, pw = _route(l[i:i + 2000], k, mask=mask[i:i + 2000].clone(), **kw)
+        assert torch.equal(idx[i:i + 2000], pi)
+        assert torch.all((w[i:i + 2000] - pw).abs() <= 2 * W_RTOL * pw)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_routing_layouts_streams_and_graphs(dtype):
     """Rows at odd offsets and strides give what dense ones give; captured and
