@@ -501,8 +501,9 @@ moe_status moe_backward_grouped(const moe_config* cfg, const moe_group_opts* gro
  * gives zeros, one with a NaN or an infinity gives NaN.
  * Precision: fp32 sums, the norm in fp64.  dtype_out MOE_F32: products of
  * operands held to 22 bits, results within a few 1e-6 of the exact iterate
- * (2-norm, relative).  MOE_BF16: products of operands rounded to 11 bits,
- * results within about 1e-3 before their rounding to bf16. */
+ * (2-norm, relative).  MOE_BF16: products of operands rounded to 11 bits (22
+ * where rows or cols are below 64), results within about 1e-3 before their
+ * rounding to bf16. */
 typedef struct {
   int32_t batch;       /* matrices, 0..65535 (0: a no-op)                     */
   int32_t rows, cols;  /* of each, 1..65536                                   */

@@ -55,6 +55,7 @@ class MoELayer:
         self.topk_w = torch.empty((T, k), dtype=torch.float32, **kw)
         self.counts = torch.empty((E,), dtype=torch.int32, **kw)
         self.ws = torch.empty((max(B.moe_workspace_size(self.cfg), 256),), dtype=torch.uint8, **kw)
+        self.ows = []
 
     # ----------------------------------------------------------------- calls
     def forward(self, x: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
@@ -117,7 +118,8 @@ class MoELayer:
                       eps=1e-7, scale=1.0, stream=None) -> Dict[str, torch.Tensor]:
         """Muon's update directions (moe_orthogonalize) of the weight gradients or
         momenta in ``grads`` (the dw* of backward(), by their names), each in
-        its own dtype; a stacked [E, out, in] tensor is E matrices."""
+        its own dtype; a stacked [E, out, in] tensor is E matrices.  The layer's
+        calls share one workspace: not on two streams at once."""
         jobs, need = [], 0
         for k, g in grads.items():
             if not k.startswith("dw"):
@@ -127,12 +129,14 @@ class MoELayer:
             cfg = B.make_ortho_config(b, r, c, dt, dt, steps, coeffs, eps, scale)
             need = max(need, B.moe_orthogonalize_workspace_size(cfg))
             jobs.append((k, g, cfg))
-        if jobs and (not hasattr(self, "ows") or self.ows.numel() < need):
-            self.ows = torch.empty((max(need, 256),), dtype=torch.uint8, device=self.device)
+        if jobs and (not self.ows or self.ows[-1].numel() < need):
+            # the outgrown ones stay: a captured graph, or work queued on
+            # another stream, may still use them
+            self.ows.append(torch.empty((max(need, 256),), dtype=torch.uint8, device=self.device))
         out = {}
         for k, g, cfg in jobs:
             out[k] = torch.empty_like(g)
-            B.moe_orthogonalize(cfg, g, out[k], self.ows, stream=stream)
+            B.moe_orthogonalize(cfg, g, out[k], self.ows[-1], stream=stream)
         return out
 
     def bias_update(self, counts: Optional[torch.Tensor] = None, rate=1e-3, starved_frac=0.1,

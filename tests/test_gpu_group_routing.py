@@ -663,6 +663,27 @@ def test_layer_step_with_groups(name, padded):
                 assert _ortho_err(uu[i:i + 1], gg[i:i + 1]) <= 2 * O_TOL[u.dtype]
 
 
+def test_layer_update_keeps_what_a_graph_uses():
+    """A captured update goes on with its workspace after a larger one."""
+    layer = _layer("softmax")[2]
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    small = {"dw_router": torch.randn(140, 200, generator=gen, device="cuda")}
+    large = {"dw1": torch.randn(20, 300, 320, generator=gen, device="cuda")}
+    want = layer.orthogonalize(small)["dw_router"].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = layer.orthogonalize(small)["dw_router"]
+    n = layer.ows[-1].numel()
+    layer.orthogonalize(large)
+    assert layer.ows[-1].numel() > n
+    fill = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    got.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    assert all(bool((f == 255).all()) for f in fill)
+
+
 def test_layer_with_groups_fp32():
     shape = I.WORKLOADS["tiny"]
     host = I.make_inputs(shape)
