@@ -795,8 +795,8 @@ ns_gemm_kernel(const __grid_constant__ NsMaps maps, const NsArgs args) {
 }
 
 // ------------------------------------------- up to 128 rows: one launch in all
-// A matrix with m <= 128 (and n <= 2048) stays in the shared memory of one
-// cluster for the whole iteration: CTA `rank` of CL holds the columns
+// A matrix with m <= 128 and n <= 2048 (one or two of them: n <= 4096) stays in
+// the shared memory of one cluster for the whole iteration: CTA `rank` of CL holds the columns
 // [64 nbx rank, 64 nbx (rank + 1)) of X, and every CTA all of A and B, as pairs of
 // planes in boxes of 128 rows x 64 columns (one layout serves as the
 // K-major operands of the gram and poly products and as the MN-major one of
@@ -810,8 +810,8 @@ ns_gemm_kernel(const __grid_constant__ NsMaps maps, const NsArgs args) {
 // What bounds it is latency: the products of one tile (24 with three terms, 8
 // with one, at 90 cycles), their epilogues' conversions, four block barriers and
 // three cluster barriers a step with their exchanges ([128, 128] fp32 39.5 us;
-// [100, 192] 46.7 us, bf16 31.1); 17 launches of the tiled kernel, 4 us each with all their
-// loads and stores, become one.
+// [100, 192] 46.7 us, bf16 31.1); 17 launches of the tiled kernel, 4 us each with
+// all their loads and stores, become one.
 constexpr int CL_ROWS = 128;
 constexpr int CL_BOX = CL_ROWS * 128;            // bytes of a box's plane
 constexpr int CL_MAX_BOXES = 4;                  // of X per CTA
@@ -1562,15 +1562,20 @@ OrthoLayout ortho_layout(const OrthoShape& s) {
 // cluster of eight waits for another to end (16 of [100, 1024] bf16: 91 us on
 // eight CTAs each, 53 on four).  16 CTAs, more than a cluster is sure to get,
 // only for single matrices wider than 8 of them take so ([128, 2048] fp32: 85 us
-// on 8 CTAs, 72 us on 16).
+// on 8 CTAs, 72 us on 16; [128, 4096], which needs 16, 92 us and 137 by the tiled
+// kernel).
 int cluster_size(int batch, int m, int n) {
-  if (m > CL_ROWS || n > 8 * CL_MAX_BOXES * 64) return 0;
+  if (m > CL_ROWS) return 0;
   const int boxes = (n + 63) / 64;
   if (boxes <= CL_MAX_BOXES) return 1;
   if (boxes <= 8) return batch <= 32 ? 4 : 2;
   if (boxes <= 16) return batch <= 12 ? 8 : 4;
-  return batch <= 2 ? 16 : 8;
+  if (batch <= 2 && boxes <= 16 * CL_MAX_BOXES) return 16;
+  return boxes <= 8 * CL_MAX_BOXES ? 8 : 0;
 }
+
+// Can eight CTAs take the matrix where a cluster of 16 is not to be had?
+bool fits_eight(int n) { return n <= 8 * CL_MAX_BOXES * 64; }
 
 template <typename T, bool TRANS, int CL, int TERMS>
 cudaError_t launch_cluster(const ClArgs& args, int smem, cudaStream_t stream) {
@@ -1656,7 +1661,9 @@ cudaError_t run_cluster(const OrthoShape& s, int cl, const void* g, void* out, v
   if (cl == 16) {
     const cudaError_t e = trans ? launch_cluster<T, true, 16, TERMS>(a, smem, stream)
                                 : launch_cluster<T, false, 16, TERMS>(a, smem, stream);
-    return e == cudaErrorInvalidConfiguration ? run_cluster<T, TERMS>(s, 8, g, out, ws, stream) : e;
+    if (e == cudaSuccess) return e;
+    cudaGetLastError();   // not left for the caller's next check: 8 CTAs, or tiles, do as well
+    return fits_eight(a.n) ? run_cluster<T, TERMS>(s, 8, g, out, ws, stream) : e;
   }
   auto go = [&](auto one, auto two, auto four, auto eight) {
     return cl == 1 ? one(a, smem, stream)
@@ -1902,19 +1909,23 @@ cudaError_t run_init(const OrthoShape& s, const T* g, void* ws, cudaStream_t str
 
 size_t ortho_workspace(const OrthoShape& s) {
   const int m = s.rows < s.cols ? s.rows : s.cols, n = s.rows < s.cols ? s.cols : s.rows;
-  return cluster_size(s.batch, m, n) > 0 ? 256 : ortho_layout(s).total;   // 256: the status
+  return cluster_size(s.batch, m, n) > 0 && fits_eight(n) ? 256   // the status
+                                                          : ortho_layout(s).total;
 }
 
 cudaError_t orthogonalize(const OrthoShape& s, const void* g, void* out, void* ws,
                           cudaStream_t stream) {
   const int m = s.rows < s.cols ? s.rows : s.cols, n = s.rows < s.cols ? s.cols : s.rows;
   const int cl = cluster_size(s.batch, m, n);
-  if (cl > 0)
-    return three_terms(s)
-               ? (s.in_bf16 ? run_cluster<__nv_bfloat16, 3>(s, cl, g, out, ws, stream)
-                            : run_cluster<float, 3>(s, cl, g, out, ws, stream))
-               : (s.in_bf16 ? run_cluster<__nv_bfloat16, 1>(s, cl, g, out, ws, stream)
-                            : run_cluster<float, 1>(s, cl, g, out, ws, stream));
+  if (cl > 0) {
+    const cudaError_t ec =
+        three_terms(s)
+            ? (s.in_bf16 ? run_cluster<__nv_bfloat16, 3>(s, cl, g, out, ws, stream)
+                         : run_cluster<float, 3>(s, cl, g, out, ws, stream))
+            : (s.in_bf16 ? run_cluster<__nv_bfloat16, 1>(s, cl, g, out, ws, stream)
+                         : run_cluster<float, 1>(s, cl, g, out, ws, stream));
+    if (ec == cudaSuccess || fits_eight(n)) return ec;
+  }
   cudaError_t e = s.in_bf16 ? run_init(s, static_cast<const __nv_bfloat16*>(g), ws, stream)
                             : run_init(s, static_cast<const float*>(g), ws, stream);
   if (e != cudaSuccess) return e;

@@ -454,7 +454,8 @@ BATCHES = [(20, 400, 400), (9, 510, 510), (64, 250, 287), (64, 250, 250), (3, 90
            (150, 100, 250), (40, 70, 600), (5, 128, 129), (2, 129, 128), (1, 3, 2048),
            (1, 512, 2048), (2, 256, 1024), (1, 130, 3000), (2, 3000, 140), (1, 513, 515),
            (40, 70, 500), (33, 260, 90), (4, 66, 400), (13, 1000, 90), (12, 90, 1000),
-           (13, 1025, 65), (70, 64, 256)]
+           (13, 1025, 65), (70, 64, 256), (3, 100, 2000), (1, 120, 4096), (2, 4000, 66),
+           (3, 40, 2500), (1, 128, 4100)]
 
 
 @pytest.mark.parametrize("shape", BATCHES, ids=str)
