@@ -831,9 +831,17 @@ struct ClArgs {
   uint32_t* status;
 };
 
-__device__ __forceinline__ void st_cluster(uint32_t addr, const uint4& v) {
-  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};"
-               ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+template <int N>
+__device__ __forceinline__ void st_cluster(uint32_t addr, const uint32_t (&v)[N]) {
+  static_assert(N == 1 || N == 2 || N == 4, "words of a store");
+  if constexpr (N == 4)
+    asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};"
+                 ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+  else if constexpr (N == 2)
+    asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};"
+                 ::"r"(addr), "r"(v[0]), "r"(v[1]) : "memory");
+  else
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v[0]) : "memory");
 }
 __device__ __forceinline__ void st_cluster_f64(uint32_t addr, double v) {
   asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
@@ -851,17 +859,20 @@ __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) {
   return __bfloat162float(v);
 }
 
+// Splits 2 values into words of the two planes.
+__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(x, y);
+  const float2 f = __half22float2(h);
+  hi = half2_bits(h);
+  lo = half2_bits(__floats2half2_rn(x - f.x, y - f.y));
+}
+
 // Splits 8 values into 16-byte pieces of the two planes.
 __device__ __forceinline__ void split8(const float* v, uint4& hi, uint4& lo) {
   uint32_t* wh = reinterpret_cast<uint32_t*>(&hi);
   uint32_t* wl = reinterpret_cast<uint32_t*>(&lo);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-    const float2 f = __half22float2(h);
-    wh[i] = half2_bits(h);
-    wl[i] = half2_bits(__floats2half2_rn(v[2 * i] - f.x, v[2 * i + 1] - f.y));
-  }
+  for (int i = 0; i < 4; ++i) split2(v[2 * i], v[2 * i + 1], wh[i], wl[i]);
 }
 
 // v = beta (hi + lo) + v over 8 elements of a row (PAIR; else of hi alone).
@@ -1076,36 +1087,43 @@ ns_cluster_kernel(const ClArgs args) {
       }
       tc_fence_before();
       cluster_sync_all();
-      constexpr int PER = (R * 16 + CL_THREADS - 1) / CL_THREADS;   // 8-column pieces
-      float f[PER][8];
+      // Every thread adds up a piece of the CTA's rows: 8 columns, or fewer so
+      // that all threads have one.
+      constexpr int PW = CL >= 4 ? 32 / CL : 8, PIECES = CL_ROWS / PW;
+      constexpr int PER = R * PIECES / CL_THREADS;
+      float f[PER][PW];
 #pragma unroll
       for (int u = 0; u < PER; ++u) {
-        const int item = u * CL_THREADS + tid, rr = item >> 4, cc = (item & 15) * 8;
+        const int item = u * CL_THREADS + tid, rr = item / PIECES, cc = item % PIECES * PW;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[u][i] = 0.f;
-        if (rr < R && static_cast<int>(rank) * R + rr < mp && cc < mp)
+        for (int i = 0; i < PW; ++i) f[u][i] = 0.f;
+        if (static_cast<int>(rank) * R + rr < mp && cc < mp)
 #pragma unroll
           for (int s = 0; s < CL; ++s) {
-            const float4* p =
-                reinterpret_cast<const float4*>(recv + (s * R + rr) * CL_ROWS + cc);
-            const float4 x = p[0], y = p[1];
-            f[u][0] += x.x; f[u][1] += x.y; f[u][2] += x.z; f[u][3] += x.w;
-            f[u][4] += y.x; f[u][5] += y.y; f[u][6] += y.z; f[u][7] += y.w;
+            const float2* p =
+                reinterpret_cast<const float2*>(recv + (s * R + rr) * CL_ROWS + cc);
+#pragma unroll
+            for (int i = 0; i < PW / 2; ++i) {
+              const float2 x = p[i];
+              f[u][2 * i] += x.x;
+              f[u][2 * i + 1] += x.y;
+            }
           }
       }
       if (!args.recv_apart) cluster_sync_all();    // the sums are out of A's place
 #pragma unroll
       for (int u = 0; u < PER; ++u) {
-        const int item = u * CL_THREADS + tid, rr = item >> 4, cc = (item & 15) * 8;
+        const int item = u * CL_THREADS + tid, rr = item / PIECES, cc = item % PIECES * PW;
         const int r = static_cast<int>(rank) * R + rr;
         // the rows and columns the products read
-        if (rr >= R || (cc >= mp && r >= mp)) continue;
+        if (cc >= mp && r >= mp) continue;
+        uint32_t hi[PW / 2], lo[PW / 2];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[u][i] *= alpha;
-        uint4 hi, lo;
-        split8(f[u], hi, lo);
-        const uint32_t ph = smem_u32(piece(ah + (cc >> 6) * CL_BOX, r, (cc & 63) >> 3));
-        const uint32_t pl = smem_u32(piece(al + (cc >> 6) * CL_BOX, r, (cc & 63) >> 3));
+        for (int i = 0; i < PW / 2; ++i)
+          split2(alpha * f[u][2 * i], alpha * f[u][2 * i + 1], hi[i], lo[i]);
+        const uint32_t off = (cc & 7) * 2;
+        const uint32_t ph = smem_u32(piece(ah + (cc >> 6) * CL_BOX, r, (cc & 63) >> 3)) + off;
+        const uint32_t pl = smem_u32(piece(al + (cc >> 6) * CL_BOX, r, (cc & 63) >> 3)) + off;
 #pragma unroll
         for (uint32_t i = 0; i < CL; ++i) {
           const uint32_t t = (rank + i) % CL;      // not all to one CTA at a time
