@@ -761,3 +761,14 @@ def test_binding_refuses_tensors_it_cannot_pass_on():
             B.moe_orthogonalize(oc, g, out, ws)
     torch.cuda.synchronize()
     assert torch.all(idx == -7) and torch.all(w == -7.0) and torch.all(dl == -7.0)
+
+
+def test_orthogonalize_refuses_a_workspace_on_the_host():
+    g = torch.randn(1, 200, 200, device="cuda")
+    out = torch.full_like(g, -7.0)
+    oc = B.make_ortho_config(1, 200, 200, B.DTYPE_F32, B.DTYPE_F32)
+    ws = torch.empty(B.moe_orthogonalize_workspace_size(oc) + 256, dtype=torch.uint8)
+    with pytest.raises(B.MoEError):
+        B.moe_orthogonalize(oc, g, out, ws[(-ws.data_ptr()) % 256:])
+    torch.cuda.synchronize()
+    assert torch.all(out == -7.0)
