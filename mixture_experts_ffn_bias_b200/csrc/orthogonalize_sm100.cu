@@ -1580,7 +1580,7 @@ OrthoLayout ortho_layout(const OrthoShape& s) {
 // cluster of eight waits for another to end (16 of [100, 1024] bf16: 91 us on
 // eight CTAs each, 53 on four).  16 CTAs, more than a cluster is sure to get,
 // only for single matrices wider than 8 of them take so ([128, 2048] fp32: 85 us
-// on 8 CTAs, 72 us on 16; [128, 4096], which needs 16, 92 us and 137 by the tiled
+// on 8 CTAs, 71 us on 16; [128, 4096], which needs 16, 91 us and 137 by the tiled
 // kernel).
 int cluster_size(int batch, int m, int n) {
   if (m > CL_ROWS) return 0;
