@@ -499,11 +499,18 @@ moe_status moe_backward_grouped(const moe_config* cfg, const moe_group_opts* gro
  *   out = scale * X                    (transposed back)
  * The matrices of the batch do not affect one another; a matrix of zeros
  * gives zeros, one with a NaN or an infinity gives NaN.
- * Precision: fp32 sums, the norm in fp64.  dtype_out MOE_F32: products of
- * operands held to 22 bits, results within a few 1e-6 of the exact iterate
- * (2-norm, relative).  MOE_BF16: products of operands rounded to 11 bits (22
- * where rows or cols are below 64), results within about 1e-3 before their
- * rounding to bf16. */
+ * Precision: fp32 sums, the norm in fp64, operands of the products held to 22
+ * bits; to 11 bits where dtype_out is MOE_BF16, rows and cols are at least 64,
+ * and the errors this leaves stay bounded over the steps of the polynomial
+ * (the usual one: up to 5 steps; (2, -1.5, 0.5) or (3, -3.2, 1.2): any).
+ * Errors relative to the exact iterate (2-norm of the whole matrix), before the
+ * rounding to dtype_out, with the usual polynomial:
+ *   22 bits  1e-6 to 2e-5 at 5 steps, up to 6e-5 at 6 and 4e-4 at 9.  Directions
+ *            whose singular value is below about 1e-7 of the norm are noise,
+ *            which grows a-fold per step as they do.
+ *   11 bits  1e-3 to 3e-3 at 5 steps, less at fewer; up to 1.2e-2 where equal
+ *            singular values meet sparse singular vectors (a scaled identity),
+ *            whose roundings do not average out. */
 typedef struct {
   int32_t batch;       /* matrices, 0..65535 (0: a no-op)                     */
   int32_t rows, cols;  /* of each, 1..65536                                   */

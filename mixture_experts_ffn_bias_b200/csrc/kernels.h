@@ -242,7 +242,10 @@ struct OrthoShape {
   int steps;
   float a, b, c, eps, scale;
   long long g_ld, g_bs, out_ld, out_bs;
+  int three_terms;           // ortho_three_terms of the rest
 };
+// Products of three terms (pairs of planes), or of the high planes alone.
+bool ortho_three_terms(const OrthoShape& s);
 size_t ortho_workspace(const OrthoShape& s);
 bool ortho_coeffs_ok(float a, float b, float c, int steps);
 cudaError_t orthogonalize(const OrthoShape& s, const void* g, void* out, void* ws,

@@ -602,6 +602,7 @@ moe_status ortho_shape(const moe_ortho_config* c, moe::OrthoShape* s) {
     *dst[i + 1] = bs;
   }
   if (!moe::ortho_coeffs_ok(c->a, c->b, c->c, c->steps)) return MOE_ERR_UNSUPPORTED;
+  s->three_terms = moe::ortho_three_terms(*s);
   return MOE_OK;
 }
 

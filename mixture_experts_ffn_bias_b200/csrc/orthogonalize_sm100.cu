@@ -16,7 +16,7 @@
 // nothing overflows, and the small elements of early iterates stay out of
 // fp16's subnormals); products accumulate in fp32.  Each value v is kept as
 // hi = fp16(v) and, where it counts, lo = fp16(v - hi), 22 bits together.
-//   TERMS = 3  (fp32 results) every product is hi lo + lo hi + hi hi and all
+//   TERMS = 3  (fp32 results, and bf16 ones of more steps) every product is hi lo + lo hi + hi hi and all
 //              of X, A, B are pairs.  The tensor cores' accumulator does not
 //              round to nearest, and its error grows with the inner
 //              dimension (1.7e-5 of the result at n = 2048), so it takes 256
@@ -29,8 +29,16 @@
 //              11 bits there would grow with them (relative error 3e-2 on
 //              matrices of low rank against 1e-3 with the pair, simulated);
 //              in the last step they grow no further, and lo times a without
-//              lo times B would add error to the large ones.  The error of
-//              the result, 1e-3, is below the rounding to bf16, 1.7e-3.
+//              lo times B would add error to the large ones.  Simulated with
+//              exact sums, Muon's polynomial, five steps, ten spectra from 64 x
+//              64 to 640 x 1024: 0.2e-3 to 2.9e-3 of the result before its
+//              rounding to bf16 (1.7e-3); six steps 4.6e-3, nine 1.3e-2, 32
+//              steps 3.9e-2.  Roundings average out less where singular
+//              vectors are sparse: a scaled identity of rank 43 1.2e-2 at five
+//              steps.  Muon's polynomial moves the values near 1 about for
+//              ever and multiplies errors as it goes, so one term is for
+//              polynomials and steps that one_term_holds() accepts: Muon's up
+//              to five steps, converging ones at any number.
 //              Matrices with m < 64 take three terms all the same: few
 //              elements do not average the 11 bits' roundings out (7e-3 seen
 //              on a 1 x 1 matrix), and their products cost next to nothing.
@@ -1536,9 +1544,33 @@ cudaError_t launch_ns(const NsMaps& maps, NsArgs args, cudaStream_t stream) {
 inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 inline long long pad64(int v) { return (static_cast<long long>(v) + 63) / 64 * 64; }
 
-// Products of three terms (pairs of planes) or of the high planes alone.
-bool three_terms(const OrthoShape& s) {
-  return !s.out_bf16 || (s.rows < s.cols ? s.rows : s.cols) < 64;
+// Do products of one term keep the directions' errors bounded?  A singular
+// value x becomes x' = x (a + q) with q = b y + c y^2, y = x^2.  In a step its
+// relative error e grows by |x p'(x) / p(x)|, and the roundings of X's hi plane,
+// of A and of B, 2^-12 each in the mean of their range, add 2 |b y + 2 c y^2| + |q|
+// of it, by x / x'.  The largest sum over values from 2^-8 (smaller ones are still
+// in the polynomial's linear part) to 1 is compared with 100, 2.4e-2: Muon's
+// polynomial has 92 after five steps and 138 after six, (3, -3.2, 1.2) never more than
+// 9, (2, -1.5, 0.5) 2.  A simulation of 1 x 1 matrices finds 98, 141, 13.7 and 2.
+// About 1 us on the host for five steps.
+bool one_term_holds(float a, float b, float c, int steps) {
+  constexpr int N = 128;
+  float x[N], e[N];
+  for (int i = 0; i < N; ++i) {
+    x[i] = i == 0 ? 1.f : x[i - 1] * 0.95760328f;   // 2^(-8 / N)
+    e[i] = 0.f;
+  }
+  for (int s = 0; s < steps; ++s)
+    for (int i = 0; i < N; ++i) {
+      const float y = x[i] * x[i], q = b * y + c * y * y;
+      const float grow = a + 3.f * b * y + 5.f * c * y * y;
+      const float add = 2.f * std::fabs(b * y + 2.f * c * y * y) + std::fabs(q);
+      e[i] = (std::fabs(grow) * e[i] + add) / std::fabs(a + q);
+      x[i] = std::fabs(x[i] * (a + q));
+    }
+  for (int i = 0; i < N; ++i)
+    if (!(e[i] <= 100.f)) return false;   // a value that became 0 as well
+  return true;
 }
 
 struct OrthoLayout {
@@ -1555,7 +1587,6 @@ OrthoLayout ortho_layout(const OrthoShape& s) {
   const int m = s.rows < s.cols ? s.rows : s.cols, n = s.rows < s.cols ? s.cols : s.rows;
   const size_t x = static_cast<size_t>(s.batch) * m * pad64(n) * 2;
   const size_t a = static_cast<size_t>(s.batch) * m * pad64(m) * 2;
-  const bool pairs = three_terms(s);
   OrthoLayout L{};
   size_t o = 0;
   L.status = o;  o += 256;
@@ -1565,9 +1596,9 @@ OrthoLayout ortho_layout(const OrthoShape& s) {
     L.xl[i] = o; o += up256(x);
   }
   L.ah = o; o += up256(a);
-  L.al = o; o += pairs ? up256(a) : 0;
+  L.al = o; o += s.three_terms ? up256(a) : 0;
   L.bh = o; o += up256(a);
-  L.bl = o; o += pairs ? up256(a) : 0;
+  L.bl = o; o += s.three_terms ? up256(a) : 0;
   L.total = o;
   return L;
 }
@@ -1925,6 +1956,11 @@ cudaError_t run_init(const OrthoShape& s, const T* g, void* ws, cudaStream_t str
 
 }  // namespace
 
+bool ortho_three_terms(const OrthoShape& s) {
+  return !s.out_bf16 || (s.rows < s.cols ? s.rows : s.cols) < 64 ||
+         !one_term_holds(s.a, s.b, s.c, s.steps);
+}
+
 size_t ortho_workspace(const OrthoShape& s) {
   const int m = s.rows < s.cols ? s.rows : s.cols, n = s.rows < s.cols ? s.cols : s.rows;
   return cluster_size(s.batch, m, n) > 0 && fits_eight(n) ? 256   // the status
@@ -1937,7 +1973,7 @@ cudaError_t orthogonalize(const OrthoShape& s, const void* g, void* out, void* w
   const int cl = cluster_size(s.batch, m, n);
   if (cl > 0) {
     const cudaError_t ec =
-        three_terms(s)
+        s.three_terms
             ? (s.in_bf16 ? run_cluster<__nv_bfloat16, 3>(s, cl, g, out, ws, stream)
                          : run_cluster<float, 3>(s, cl, g, out, ws, stream))
             : (s.in_bf16 ? run_cluster<__nv_bfloat16, 1>(s, cl, g, out, ws, stream)
@@ -1947,7 +1983,7 @@ cudaError_t orthogonalize(const OrthoShape& s, const void* g, void* out, void* w
   cudaError_t e = s.in_bf16 ? run_init(s, static_cast<const __nv_bfloat16*>(g), ws, stream)
                             : run_init(s, static_cast<const float*>(g), ws, stream);
   if (e != cudaSuccess) return e;
-  return three_terms(s) ? run_steps<3>(s, out, ws, stream) : run_steps<1>(s, out, ws, stream);
+  return s.three_terms ? run_steps<3>(s, out, ws, stream) : run_steps<1>(s, out, ws, stream);
 }
 
 // The polynomial p(x) = a x + b x^3 + c x^5 keeps the fp16 planes in range

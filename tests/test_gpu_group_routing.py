@@ -772,3 +772,40 @@ def test_orthogonalize_refuses_a_workspace_on_the_host():
         B.moe_orthogonalize(oc, g, out, ws[(-ws.data_ptr()) % 256:])
     torch.cuda.synchronize()
     assert torch.all(out == -7.0)
+
+
+def _equal_values(rank, rows, cols, seed):
+    """A matrix of `rank` equal singular values with random singular vectors."""
+    g = torch.Generator().manual_seed(seed)
+    u = torch.linalg.qr(torch.randn(rows, rank, generator=g, dtype=torch.float64))[0]
+    v = torch.linalg.qr(torch.randn(cols, rank, generator=g, dtype=torch.float64))[0]
+    return (u @ v.T)[None].float().cuda()
+
+
+@pytest.mark.parametrize("rows,cols", [(333, 517), (517, 333), (700, 900), (100, 300), (96, 96),
+                                       (128, 2500)])
+@pytest.mark.parametrize("steps,coeffs,grow", [
+    (6, B.MUON_COEFFS, 150), (9, B.MUON_COEFFS, 520), (5, (3.7418, -5.5913, 2.3037), 480)])
+def test_orthogonalize_bf16_of_many_steps(rows, cols, steps, coeffs, grow):
+    """More steps than products of one term bear ([333, 517] so: 4.6e-3 and 1.3e-2
+    at 6 and 9 steps).  grow: the relative error's largest growth over the steps
+    (1 x 1 matrices, simulated); 22-bit operands and fp32 sums leave about 1e-6 of
+    the iterate a step, and the result is rounded by at most 2^-8."""
+    g = _equal_values(min(rows, cols), rows, cols, rows + cols)
+    out, ws = _ortho(g, torch.bfloat16, steps=steps, coeffs=coeffs)
+    assert B.moe_device_status(ws) == (B.MOE_OK, 0)
+    assert _ortho_err(out, g, steps=steps, coeffs=coeffs) <= 2.0 ** -8 + 1e-6 * grow
+
+
+@pytest.mark.parametrize("rows,cols", [(64, 96), (333, 517)])
+def test_orthogonalize_roundings_that_coincide(rows, cols):
+    """A scaled identity of rank 43, whose elements all round alike: products of
+    one term stay within the bound that admits them, 100 2^-12, and 22 bits
+    within as many of theirs."""
+    g = torch.zeros(1, rows, cols, device="cuda")
+    i = torch.arange(43, device="cuda")
+    g[0, i, i] = 0.37
+    out, _ = _ortho(g, torch.bfloat16)
+    assert _ortho_err(out, g) <= 100 * 2.0 ** -12 + 2.0 ** -8
+    out, _ = _ortho(g, torch.float32)
+    assert _ortho_err(out, g) <= 100 * 2.0 ** -22 + 5 * 1e-6

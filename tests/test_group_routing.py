@@ -231,3 +231,20 @@ def test_orthogonalize_arguments_refused(lib):
             run(bad, g, ws)
     empty = B.make_ortho_config(0, 32, 48)
     assert lib.moe_orthogonalize(ctypes.byref(empty), None, None, None, 0, None) == B.MOE_OK
+
+
+def test_orthogonalize_terms_by_the_growth_of_errors(lib):
+    """bf16 results of products of one term only where the errors those leave
+    stay bounded: the planes a workspace has room for tell which are taken."""
+    size = lambda **kw: B.moe_orthogonalize_workspace_size(
+        B.make_ortho_config(3, 333, 517, **kw))
+    pairs = lambda **kw: size(**kw) == size(**{**kw, "out_dtype": B.DTYPE_F32})
+    assert not any(pairs(steps=n) for n in range(1, 6))
+    assert all(pairs(steps=n) for n in range(6, 33))
+    for coeffs in ((2.0, -1.5, 0.5), (1.5, -0.5, 0.0), (3.0, -3.2, 1.2), (1.875, -1.25, 0.375)):
+        assert not any(pairs(steps=n, coeffs=coeffs) for n in (1, 5, 8, 32)), coeffs
+    # steeper than the usual polynomial
+    assert pairs(steps=4, coeffs=(3.7418, -5.5913, 2.3037))
+    assert pairs(steps=2, coeffs=(4.0848, -6.8946, 2.9270))
+    # a value that becomes zero on the way: its direction has no relative error
+    assert pairs(steps=2, coeffs=(1.0, -1.0, 0.0))
