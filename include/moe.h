@@ -526,7 +526,8 @@ typedef struct {
   int64_t out_row_stride, out_batch_stride;  /* in elements; 0: dense        */
 } moe_ortho_config;
 
-/* Bytes of workspace of moe_orthogonalize (0 on an invalid configuration). */
+/* Bytes of workspace of moe_orthogonalize (0 on an invalid configuration;
+ * at least 256 else, for batch 0 too). */
 size_t moe_orthogonalize_workspace_size(const moe_ortho_config* cfg);
 
 /* g [batch, rows, cols] of dtype_in -> out, the same shape, of dtype_out; the

@@ -1962,6 +1962,7 @@ bool ortho_three_terms(const OrthoShape& s) {
 }
 
 size_t ortho_workspace(const OrthoShape& s) {
+  if (s.batch == 0) return 256;   // the call does nothing; no layout of no matrices
   const int m = s.rows < s.cols ? s.rows : s.cols, n = s.rows < s.cols ? s.cols : s.rows;
   return cluster_size(s.batch, m, n) > 0 && fits_eight(n) ? 256   // the status
                                                           : ortho_layout(s).total;

@@ -248,3 +248,16 @@ def test_orthogonalize_terms_by_the_growth_of_errors(lib):
     assert pairs(steps=2, coeffs=(4.0848, -6.8946, 2.9270))
     # a value that becomes zero on the way: its direction has no relative error
     assert pairs(steps=2, coeffs=(1.0, -1.0, 0.0))
+
+
+@pytest.mark.parametrize("rows,cols", [(333, 517), (130, 130), (100, 5000), (5000, 100), (1, 1),
+                                       (100, 200), (65536, 65536)])
+@pytest.mark.parametrize("out_dtype", [B.DTYPE_F32, B.DTYPE_BF16])
+def test_orthogonalize_of_no_matrices(lib, rows, cols, out_dtype):
+    """An empty batch has a workspace size like any other, and is a no-op."""
+    cfg = B.make_ortho_config(0, rows, cols, out_dtype=out_dtype)
+    n = B.moe_orthogonalize_workspace_size(cfg)
+    assert n == 256
+    g = _Addr((0, rows, cols))
+    assert B.moe_orthogonalize(cfg, g, g, _Addr(nbytes=n), stream=0) == B.MOE_OK
+    assert B.moe_orthogonalize(cfg, g, g, None, stream=0) == B.MOE_OK
