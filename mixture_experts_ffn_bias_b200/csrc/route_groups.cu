@@ -26,6 +26,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cstdint>
 #include <type_traits>
 
@@ -436,8 +437,10 @@ route_kernel(const RouteShape a, const L* __restrict__ logits, const float* __re
         } else {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            odd = odd || !(v[c] <= 1e30f);        // NaN or +inf
-            v[c] = v[c] > ninf ? v[c] + bv[c] : ninf;
+            const float key = v[c] + bv[c];
+            // NaN, +inf, or two finite terms whose sum leaves fp32's range
+            odd = odd || !(v[c] <= 1e30f) || (key == ninf && v[c] > ninf && bv[c] > ninf);
+            v[c] = v[c] > ninf ? key : ninf;
           }
         }
       } else {
@@ -505,7 +508,11 @@ route_kernel(const RouteShape a, const L* __restrict__ logits, const float* __re
         if (two) sc = m1 + m2;
         err = 2.f * key_err + 1.5e-7f * (fabsf(m1) + (two ? fabsf(m2) : 0.f));
       }
-      picks[g] = make_int2(__float_as_int(err), __float_as_int(sc));
+      // A group with an eligible expert keeps a finite score and error, in the
+      // scores' order: what leaves fp32's range (a bias of +inf, sums of large
+      // ones) then lies within its error of the border, or clear of it.
+      if (m1 > ninf) sc = fminf(fmaxf(sc, -FLT_MAX), FLT_MAX);
+      picks[g] = make_int2(__float_as_int(fminf(err, FLT_MAX)), __float_as_int(sc));
     }
     __syncwarp();
     use = 0;
@@ -576,6 +583,7 @@ route_kernel(const RouteShape a, const L* __restrict__ logits, const float* __re
   // --------------------------------------------------------------- 3 top-k
   const bool alive = on && ((slow >> (8 * tok)) & 0xffu) == 0u;
   const int total = limited && whole ? a.topk_group * per : a.E;   // experts to choose from
+  const int listed = limited && whole ? __popc(use) * per : a.E;   // the same
   const int nbr = (total + 31) >> 5;               // blocks of 4 of a lane
   // The lane's blocks: where they lie in the token's keys, and their keys in
   // descending order (a block that is not there holds none).
@@ -586,7 +594,7 @@ route_kernel(const RouteShape a, const L* __restrict__ logits, const float* __re
     const int p = 4 * (nbr * sub + i);
     base[i] = 0;
     float4 q = make_float4(ninf, ninf, ninf, ninf);
-    if (alive && i < nbr && p < total) {
+    if (alive && i < nbr && p < total && p < listed) {
       int e = p;
       if (limited && whole) {
         const int gi = static_cast<int>((p + 0.5f) * inv_per);
@@ -675,16 +683,20 @@ route_kernel(const RouteShape a, const L* __restrict__ logits, const float* __re
       return to_f32<L>(row[e]) == to_f32<L>(row[f]) && bias[e] == bias[f];
     };
     bool near = false;   // two neighbours of the chosen ones
+    bool huge = false;   // keys of +inf, whose gaps and margins say nothing
     bool edge = false;   // the last of them and the best one left out
     for (int j = sub; j + 1 < count; j += 8) {
       const int2 p = picks[j], n = picks[j + 1];
       const float best = __int_as_float(p.y), gap = best - __int_as_float(n.y);
       const bool c = !(gap > margin(best)) || best < floor;
-      if (j + 1 == a.k)
+      if (best > FLT_MAX)
+        huge = true;
+      else if (j + 1 == a.k)
         edge = c && (biased || fabsf(best) < 1e-6f || best < floor);
       else if (c)
         near = near || (biased ? !same(expert_at(p.x), expert_at(n.x)) : gap > 0.f);
     }
+    slow |= __ballot_sync(kFull, huge);
     if (__any_sync(kFull, near || edge)) {
       moved = true;
       const unsigned edges = __ballot_sync(kFull, edge);
@@ -705,7 +717,7 @@ route_kernel(const RouteShape a, const L* __restrict__ logits, const float* __re
 #pragma unroll
             for (int c = 0; c < 4; ++c)
               if (biased)
-                differs = differs || (fabsf(v[c] - lk) <= margin(lk) &&
+                differs = differs || (v[c] > ninf && fabsf(v[c] - lk) <= margin(lk) &&
                                       !same(e + c, expert_at(last.x)));
               else
                 differs = differs || (v[c] != lk && v[c] > ninf &&

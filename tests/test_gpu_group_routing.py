@@ -809,3 +809,78 @@ def test_orthogonalize_roundings_that_coincide(rows, cols):
     assert _ortho_err(out, g) <= 100 * 2.0 ** -12 + 2.0 ** -8
     out, _ = _ortho(g, torch.float32)
     assert _ortho_err(out, g) <= 100 * 2.0 ** -22 + 5 * 1e-6
+
+
+@pytest.mark.parametrize("gate", [SIG, SOFT])
+@pytest.mark.parametrize("space", [0, 1])
+@pytest.mark.parametrize("score", [1, 2])
+@pytest.mark.parametrize("per", [8, 5])
+def test_routing_biases_beyond_fp32_sums(gate, space, score, per):
+    """Experts forced on by +inf or by 3e38, switched off by -3e38 or the lowest
+    value: keys, and sums of two, that leave fp32's range on either side."""
+    G, T, k = 8, 17, 6
+    E = G * per
+    rng = np.random.default_rng(10 * per + score)
+    low, high = np.finfo(np.float32).min, np.finfo(np.float32).max
+    a = rng.standard_normal((T, E)).astype(np.float32)
+    a[3, ::2] = low
+    a[4, :per] = -np.inf
+    a[5] = low
+    a[6] = -np.inf
+    a[7, 1::2] = -np.inf
+    plain = (0.1 * rng.standard_normal(E)).astype(np.float32)
+    biases = []
+    for value in (np.inf, high, 3e38, 2e38, -2e38, -3e38, low):
+        for which in ([1], [1, 2], [0, per + 1, 2 * per], range(3, E, per), range(0, E, 2),
+                      range(per, 3 * per), range(E - 3, E), range(E)):
+            b = plain.copy()
+            b[list(which)] = value
+            biases.append(b)
+    b = plain.copy()                       # both sides in one group
+    b[0], b[1], b[per], b[per + 1] = 3e38, low, -1e38, 0.0
+    biases.append(b)
+    b = plain.copy()
+    b[::3], b[1::3] = np.inf, -np.inf
+    biases.append(b)
+    b = np.full(E, low)                    # groups of the lowest beside empty ones
+    b[:per], b[2 * per:3 * per] = -np.inf, -np.inf
+    biases.append(b)
+    l = torch.from_numpy(a).cuda()
+    for b in biases:
+        for tg in (1, 3):
+            _check_nan(l, k, gate, space, torch.from_numpy(b).cuda(), tg, score)
+
+
+def test_routing_forced_expert_beside_a_close_call():
+    """An expert forced on by +inf keeps its group where two others are close."""
+    T, per, G = 64, 8, 4
+    rng = np.random.default_rng(3)
+    a = (0.01 * rng.standard_normal((T, per * G)) - 1.0).astype(np.float32)
+    a[:, 2 * per] = 0.5
+    a[:, 3 * per] = np.nextafter(np.float32(0.5), np.float32(1))
+    b = np.zeros(per * G, np.float32)
+    b[1] = np.inf
+    b[2 * per] = 3e-8
+    for gate in (SIG, SOFT):
+        for score in (1, 2):
+            for space in (0, 1):
+                out = _route(torch.from_numpy(a).cuda(), 4, gate=gate, space=space, groups=G,
+                             topk_group=2, score=score, bias=torch.from_numpy(b).cuda())
+                ri, rw, _ = O.route_groups(a, 4, gate, True, b, G, 2, score, space)
+                assert np.all(ri[:, 0] == 1)
+                np.testing.assert_array_equal(out[2].cpu().numpy(), ri)
+                assert np.all(np.abs(out[3].double().cpu().numpy() - rw) <= W_RTOL * rw)
+
+
+@pytest.mark.parametrize("E", [61, 62, 63, 64])
+def test_routing_ties_at_inf_at_the_end_of_a_row(E):
+    """The k-th and further keys +inf, rows and bias that end with the last
+    expert of a buffer: ties go to the lower ids."""
+    T, k = 5, 4
+    l = torch.zeros(T * E, device="cuda").view(T, E)
+    bias = torch.full((E,), INF, device="cuda")
+    for gate in (SIG, SOFT):
+        for space in (0, 1):
+            _, _, idx, w = _route(l, k, gate=gate, space=space, bias=bias)
+            assert torch.equal(idx.cpu(), torch.arange(k, dtype=torch.int32).expand(T, k))
+            assert torch.all((w - 0.25).abs() <= W_RTOL * 0.25)
