@@ -469,7 +469,8 @@ route_kernel(const RouteShape a, const L* __restrict__ logits, const float* __re
   // -------------------------------------------------------------- 2 groups
   if (limited) {
     // a score's fp32 error: none for the largest of unbiased logits, relative
-    // for sums of exponentials, else that of keys formed from fp32 scores
+    // for sums of exponentials (down to the subnormal ones), else that of keys
+    // formed from fp32 scores
 #pragma unroll 1
     for (int g = sub; g < a.groups; g += 8) {
       float m1 = ninf, m2 = ninf;
@@ -498,7 +499,7 @@ route_kernel(const RouteShape a, const L* __restrict__ logits, const float* __re
         if (m1 > ninf) {
           if (a.gate == 0) {
             sc = expf(m1 - row_m) + expf(m2 - row_m);
-            err = 1e-5f * sc;
+            err = 1e-5f * sc + 1e-42f;   // subnormal sums: steps of 1.4e-45
           } else {
             sc = fast_sigmoid(m1) + (two ? fast_sigmoid(m2) : 0.f);
             err = 7e-7f;

@@ -884,3 +884,22 @@ def test_routing_ties_at_inf_at_the_end_of_a_row(E):
             _, _, idx, w = _route(l, k, gate=gate, space=space, bias=bias)
             assert torch.equal(idx.cpu(), torch.arange(k, dtype=torch.int32).expand(T, k))
             assert torch.all((w - 0.25).abs() <= W_RTOL * 0.25)
+
+
+def test_routing_groups_of_subnormal_scores():
+    """Unbiased softmax scores that are fp32 subnormals, or zero there: their groups
+    rank as the fp64 sums do."""
+    per, G, T = 4, 6, 400
+    rng = np.random.default_rng(44)
+    a = (-100.0 + 6.0 * rng.uniform(-1, 1, (T, per * G)) * rng.uniform(0.01, 1, (T, 1)))
+    a[:, 0] = 0.0                        # the first group holds all the weight
+    a[:, 1:4] = -300.0
+    a[0] = [0, -300, -300, -300] + [-101.56, -101.76, -300, -300] + \
+        [-101.64, -101.64, -300, -300] + [-300] * 12
+    a[1] = [0, -300, -300, -300] + [-101.64, -101.64, -300, -300] + \
+        [-101.56, -101.76, -300, -300] + [-300] * 12
+    l = torch.from_numpy(a.astype(np.float32)).cuda()
+    for tg in (2, 4):
+        out = _route(l, 6, gate=SOFT, groups=G, topk_group=tg, score=2)
+        ri, _, _ = O.route_groups(l.double().cpu().numpy(), 6, SOFT, True, None, G, tg, 2, 1)
+        np.testing.assert_array_equal(out[2].cpu().numpy(), ri)
