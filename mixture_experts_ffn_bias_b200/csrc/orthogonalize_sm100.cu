@@ -198,6 +198,13 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
+// The two halves of cluster_sync_all.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void fence_cluster() {
   asm volatile("fence.acq_rel.cluster;" ::: "memory");
 }
@@ -936,6 +943,9 @@ ns_cluster_kernel(const ClArgs args) {
     tmem_alloc(&s_tmem, 512);
     tmem_relinquish();
   }
+  __syncwarp();
+  // a CTA's shared memory may be stored to from its start on: waited for below
+  if constexpr (CL > 1) cluster_arrive();
   pdl_wait();
   if (blockIdx.x == 0 && tid == 0) *args.status = 0u;   // the call's status starts clear
   // ------------------------------------------------------------- the norm
@@ -977,6 +987,7 @@ ns_cluster_kernel(const ClArgs args) {
   for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
   if (lane == 0) s_part[warp] = acc;
   __syncthreads();
+  if constexpr (CL > 1) cluster_wait();   // every CTA of the cluster has started
   if (tid == 0) {
     double t = 0.0;
     for (int w = 0; w < CL_THREADS / 32; ++w) t += s_part[w];
@@ -984,6 +995,7 @@ ns_cluster_kernel(const ClArgs args) {
     else
       for (uint32_t q = 0; q < CL; ++q) st_cluster_f64(map_rank(smem_u32(&s_norm[rank]), q), t);
   }
+  __syncwarp();
   tc_fence_before();
   if constexpr (CL > 1) cluster_sync_all(); else __syncthreads();
   tc_fence_after();

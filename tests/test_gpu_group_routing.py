@@ -903,3 +903,27 @@ def test_routing_groups_of_subnormal_scores():
         out = _route(l, 6, gate=SOFT, groups=G, topk_group=tg, score=2)
         ri, _, _ = O.route_groups(l.double().cpu().numpy(), 6, SOFT, True, None, G, tg, 2, 1)
         np.testing.assert_array_equal(out[2].cpu().numpy(), ri)
+
+
+# clusters of 4, 8, 16, 16, 8 and 8 CTAs, 1, 3, 7, 7, 3 and 1 of them without a column
+IDLE_CTAS = [(1, 100, 320), (2, 90, 576), (1, 128, 1088), (2, 1100, 128), (12, 580, 100),
+             (3, 100, 800)]
+
+
+@pytest.mark.parametrize("shape", IDLE_CTAS, ids=str)
+@pytest.mark.parametrize("dout", [torch.float32, torch.bfloat16])
+def test_orthogonalize_clusters_with_idle_ctas(shape, dout):
+    """CTAs without columns reach the exchange of the norm long before, or after,
+    the others: the sums are whole, call after call."""
+    gen = torch.Generator(device="cuda").manual_seed(sum(shape))
+    g = torch.randn(*shape, generator=gen, device="cuda")
+    ref = _ref64(g)
+    first = None
+    for _ in range(30):
+        out, ws = _ortho(g, dout)
+        assert B.moe_device_status(ws) == (B.MOE_OK, 0)
+        first = out if first is None else first
+        assert torch.equal(out, first)
+    err = torch.linalg.vector_norm(first.double() - ref, dim=(1, 2)) / \
+        torch.linalg.vector_norm(ref, dim=(1, 2))
+    assert err.max().item() <= O_TOL[dout]
