@@ -493,7 +493,10 @@ def _matrix_strides(t, cfg):
     row, col = t.stride()[-2:]
     if col != 1 and cfg.cols > 1:
         raise MoEError(MOE_ERR_INVALID, "the elements of a matrix row must be contiguous")
-    return (row if cfg.rows > 1 else 0), (t.stride(0) if cfg.batch > 1 else 0)
+    row, mat = row if cfg.rows > 1 else None, t.stride(0) if cfg.batch > 1 else None
+    if row == 0 or mat == 0:   # an expanded tensor; 0 would mean dense
+        raise MoEError(MOE_ERR_INVALID, f"rows or matrices share memory: strides {t.stride()}")
+    return row or 0, mat or 0
 
 
 def moe_orthogonalize(cfg, g, out, ws, stream=None, check=True) -> int:

@@ -261,3 +261,21 @@ def test_orthogonalize_of_no_matrices(lib, rows, cols, out_dtype):
     g = _Addr((0, rows, cols))
     assert B.moe_orthogonalize(cfg, g, g, _Addr(nbytes=n), stream=0) == B.MOE_OK
     assert B.moe_orthogonalize(cfg, g, g, None, stream=0) == B.MOE_OK
+
+
+def test_orthogonalize_refuses_expanded_tensors(lib):
+    """Rows or matrices of stride 0: the C call takes 0 for dense, and would read
+    or write memory the tensor does not have."""
+    cfg = B.make_ortho_config(2, 32, 48, B.DTYPE_F32, B.DTYPE_F32)
+    ws = _Addr(nbytes=B.moe_orthogonalize_workspace_size(cfg), addr=(1 << 20) + 16)   # refused
+    g = _Addr((2, 32, 48))
+    for st in ((0, 48, 1), (1536, 0, 1), (0, 0, 1)):
+        bad = _Addr((2, 32, 48), stride=st)
+        for args in ((bad, g), (g, bad)):
+            with pytest.raises(B.MoEError):
+                B.moe_orthogonalize(cfg, *args, ws, stream=0, check=False)
+    # one row, or one matrix: its stride says nothing
+    one = B.make_ortho_config(1, 1, 48, B.DTYPE_F32, B.DTYPE_F32)
+    g = _Addr((1, 1, 48), stride=(0, 0, 1))
+    assert B.moe_orthogonalize(one, g, g, _Addr(nbytes=0), stream=0, check=False) == \
+        B.MOE_ERR_WORKSPACE
