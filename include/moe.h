@@ -195,7 +195,8 @@ typedef struct {
   int32_t reserved[2];   /* 0                                               */
 } moe_group_opts;
 
-/* cfg: T, n_experts, top_k, gate and norm_topk_prob are used.
+/* cfg: T, n_experts, top_k, gate and norm_topk_prob are used, the others not
+ * looked at (a caller with logits alone may leave them 0).
  *   logits [T, E] of logits_dtype, rows of logits_ld elements (>= E);
  *   sel_bias [E] fp32 or NULL (moves the selection only; -inf switches an
  *   expert off); token_mask [T] bytes or NULL: a token with 0 (padding) gets

@@ -81,6 +81,18 @@ moe_status check_cfg(const moe_config* c) {
   return MOE_OK;
 }
 
+// The fields a router on given logits uses.
+moe_status check_routing(const moe_config* c) {
+  if (c == nullptr) return MOE_ERR_INVALID;
+  if (c->T < 0 || c->n_experts < 1 || c->top_k < 1 || c->top_k > c->n_experts)
+    return MOE_ERR_INVALID;
+  if (c->gate != MOE_GATE_SOFTMAX && c->gate != MOE_GATE_SIGMOID) return MOE_ERR_INVALID;
+  if (c->norm_topk_prob != 0 && c->norm_topk_prob != 1) return MOE_ERR_INVALID;
+  if (c->n_experts > 256 || c->top_k > 32) return MOE_ERR_UNSUPPORTED;
+  if (static_cast<long long>(c->T) * c->top_k > 0x3fffffffLL) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
 moe_status check_ws(const moe_config* c, const void* ws, size_t ws_bytes) {
   if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1))) return MOE_ERR_INVALID;
   if (ws_bytes < layout(*c).total) return MOE_ERR_WORKSPACE;
@@ -255,10 +267,12 @@ moe_status check_weights(const moe_config* c, const moe_expert_weights* w) {
   return MOE_OK;
 }
 
-// cfg and opts of a group-limited routing call -> the launcher's shape.
+// cfg and opts of a group-limited routing call -> the launcher's shape.  Of
+// cfg, what routing uses is checked: the sizes and type of a layer that only
+// has its logits routed are its own affair.
 moe_status route_shape(const moe_config* c, const moe_group_opts* o, int64_t ld,
                        moe::RouteShape* s) {
-  const moe_status st = check_cfg(c);
+  const moe_status st = check_routing(c);
   if (st != MOE_OK) return st;
   if (o == nullptr || o->n_group < 1 || o->topk_group < 1 || o->topk_group > o->n_group ||
       c->n_experts % o->n_group != 0 || (o->group_score != 1 && o->group_score != 2) ||

@@ -279,3 +279,30 @@ def test_orthogonalize_refuses_expanded_tensors(lib):
     g = _Addr((1, 1, 48), stride=(0, 0, 1))
     assert B.moe_orthogonalize(one, g, g, _Addr(nbytes=0), stream=0, check=False) == \
         B.MOE_ERR_WORKSPACE
+
+
+def test_routing_looks_at_its_own_fields_alone(lib):
+    """The sizes and type of a layer do not matter to calls on given logits: any
+    values pass, and a bad one of routing's own fields is refused beside them."""
+    o, l = B.make_group_opts(4, 2), _Addr((16, 16))
+    for other in (dict(d_model=100, d_ff=1), dict(d_model=0, d_ff=0), dict(d_model=-1, d_ff=7)):
+        cfg = B.make_config(**{**CFG, **other, "T": 0})
+        e = _Addr((0, 16))
+        assert B.moe_route_groups(cfg, o, e, None, None, None, None, stream=0) == B.MOE_OK
+        assert B.moe_route_groups_backward(cfg, o, e, None, None, e, stream=0) == B.MOE_OK
+        assert B.moe_check_config(cfg) != B.MOE_OK
+        for field, value, expect in (("top_k", 17, B.MOE_ERR_INVALID),
+                                     ("top_k", 0, B.MOE_ERR_INVALID),
+                                     ("gate", 2, B.MOE_ERR_INVALID),
+                                     ("norm_topk_prob", 2, B.MOE_ERR_INVALID),
+                                     ("T", -1, B.MOE_ERR_INVALID)):
+            bad = B.make_config(**{**CFG, **other})
+            setattr(bad, field, value)
+            g = _Addr((max(bad.T, -1), 16))
+            assert B.moe_route_groups(bad, o, g, None, None, l, l, stream=0,
+                                      check=False) == expect
+        # the layer calls look at all of them
+        cfg = B.make_config(**{**CFG, **other})
+        w = {k: l for k in ("w1", "w3", "w2")}
+        assert B.moe_forward_grouped(cfg, o, l, l, None, None, None, w, l, l, l, l,
+                                     _Addr(nbytes=1 << 30), stream=0, check=False) != B.MOE_OK
