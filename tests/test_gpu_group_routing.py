@@ -927,3 +927,25 @@ def test_orthogonalize_clusters_with_idle_ctas(shape, dout):
     err = torch.linalg.vector_norm(first.double() - ref, dim=(1, 2)) / \
         torch.linalg.vector_norm(ref, dim=(1, 2))
     assert err.max().item() <= O_TOL[dout]
+
+
+@pytest.mark.parametrize("shape", [(6, 48, 80), (6, 300, 280), (6, 100, 600), (6, 70, 90),
+                                   (6, 1200, 100), (6, 1, 40), (6, 200, 1200)], ids=str)
+@pytest.mark.parametrize("din", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("dout", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("steps", [1, 5])
+def test_orthogonalize_spreads_what_is_not_finite(shape, din, dout, steps):
+    """A matrix with a NaN or an infinity gives NaN everywhere, also where its parts
+    lie on several CTAs; the others, and zeros, are what they are alone."""
+    rng = np.random.default_rng(sum(shape))
+    g = torch.from_numpy(rng.standard_normal(shape).astype(np.float32)).cuda().to(din)
+    r, c = shape[1] - 1, shape[2] // 3
+    clean = g.clone()
+    g[0, r, c], g[1, 0, -1], g[2, r, c] = float("nan"), INF, -INF
+    g[3] = 0
+    out, ws = _ortho(g, dout, steps=steps)
+    want, _ = _ortho(clean, dout, steps=steps)
+    assert torch.isnan(out[:3]).all()
+    assert torch.all(out[3] == 0)
+    assert torch.equal(out[4:], want[4:])
+    assert B.moe_device_status(ws) == (B.MOE_OK, 0)
