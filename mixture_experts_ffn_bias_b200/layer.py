@@ -119,7 +119,9 @@ class MoELayer:
         """Muon's update directions (moe_orthogonalize) of the weight gradients or
         momenta in ``grads`` (the dw* of backward(), by their names), each in
         its own dtype; a stacked [E, out, in] tensor is E matrices.  The layer's
-        calls share one workspace: not on two streams at once."""
+        calls share one workspace: not on two streams at once.  It grows to the
+        largest set of gradients a call has had, and outgrown ones are kept with
+        the layer (a captured graph may use them): pass the largest set first."""
         jobs, need = [], 0
         for k, g in grads.items():
             if not k.startswith("dw"):
@@ -129,14 +131,24 @@ class MoELayer:
             cfg = B.make_ortho_config(b, r, c, dt, dt, steps, coeffs, eps, scale)
             need = max(need, B.moe_orthogonalize_workspace_size(cfg))
             jobs.append((k, g, cfg))
-        if jobs and (not self.ows or self.ows[-1].numel() < need):
-            # the outgrown ones stay: a captured graph, or work queued on
-            # another stream, may still use them
-            self.ows.append(torch.empty((max(need, 256),), dtype=torch.uint8, device=self.device))
-        out = {}
-        for k, g, cfg in jobs:
-            out[k] = torch.empty_like(g)
-            B.moe_orthogonalize(cfg, g, out[k], self.ows[-1], stream=stream)
+        out, here = {}, torch.cuda.current_stream(self.device)
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(
+                stream if isinstance(stream, int) else stream.cuda_stream, device=self.device)
+        # allocated on the stream that writes: a block of the current one's may
+        # still be in use by what that has queued
+        with torch.cuda.stream(here if stream is None else stream):
+            if jobs and (not self.ows or self.ows[-1].numel() < need):
+                # the outgrown ones stay: a captured graph, or work queued on
+                # another stream, may still use them
+                self.ows.append(torch.empty((max(need, 256),), dtype=torch.uint8,
+                                            device=self.device))
+            for k, g, cfg in jobs:
+                out[k] = torch.empty_like(g)
+                B.moe_orthogonalize(cfg, g, out[k], self.ows[-1])
+        if stream is not None and stream != here:
+            for u in out.values():
+                u.record_stream(here)
         return out
 
     def bias_update(self, counts: Optional[torch.Tensor] = None, rate=1e-3, starved_frac=0.1,

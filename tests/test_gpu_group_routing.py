@@ -949,3 +949,28 @@ def test_orthogonalize_spreads_what_is_not_finite(shape, din, dout, steps):
     assert torch.all(out[3] == 0)
     assert torch.equal(out[4:], want[4:])
     assert B.moe_device_status(ws) == (B.MOE_OK, 0)
+
+
+def test_layer_update_on_another_stream():
+    """Results and workspace are not in memory that the current stream's queued
+    work still uses; streams by object and by address."""
+    layer = _layer("softmax")[2]
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    grads = {"dw1": torch.randn(20, 300, 320, generator=gen, device="cuda"),
+             "dw_router": torch.randn(140, 200, generator=gen, device="cuda")}
+    want = {k: u.clone() for k, u in layer.orthogonalize(grads).items()}
+    n = layer.ows[-1].numel()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream, None):
+        layer.ows.clear()
+        torch.cuda.synchronize()
+        gone = [torch.empty_like(g) for g in grads.values()]
+        gone.append(torch.empty(n, dtype=torch.uint8, device="cuda"))
+        torch.cuda._sleep(20_000_000)           # 10 ms of the current stream's time
+        for t in gone:
+            t.fill_(7)
+        del t, gone                             # freed on the host, written later
+        got = layer.orthogonalize(grads, stream=stream)
+        torch.cuda.synchronize()
+        for k in grads:
+            assert torch.equal(got[k], want[k]), k
