@@ -974,3 +974,59 @@ def test_layer_update_on_another_stream():
         torch.cuda.synchronize()
         for k in grads:
             assert torch.equal(got[k], want[k]), k
+
+
+@pytest.mark.parametrize("name", list(LAYERS))
+@pytest.mark.parametrize("T,on", [(1, 1), (1, 0), (70, 0), (70, 1)])
+def test_layer_step_of_few_or_no_routed_tokens(name, T, on):
+    """`on` of T tokens are no padding: experts, and all of them, without rows."""
+    shape, g, tg, score, space, scale = LAYERS[name]
+    shape = shape.replace(T=T)
+    host = I.make_inputs(shape)
+    layer = MoELayer(shape, host, groups=B.make_group_opts(g, tg, score, space, scale))
+    mask = torch.zeros(T, dtype=torch.uint8, device="cuda")
+    mask[T - on:] = 1
+    layer.ws.fill_(0xff)
+    layer.forward(token_mask=mask)
+    assert layer.device_status() == (B.MOE_OK, 0)
+    idx, w = layer.topk_idx.cpu().numpy(), layer.topk_w.double().cpu().numpy()
+    assert np.all(idx[:T - on] == -1) and np.all(w[:T - on] == 0) and np.all(idx[T - on:] >= 0)
+    assert layer.counts.sum().item() == on * shape.top_k
+    logits = host["x"].astype(np.float64) @ host["w_router"].astype(np.float64).T
+    if host.get("logit_offset") is not None:
+        logits = logits + host["logit_offset"]
+    s = O.sigmoid(logits) if shape.gate == O.GATE_SIGMOID else O.softmax_rows(logits)
+    r = O.Routing(logits, s, s, idx.astype(np.int64), w, None, None)
+    ref, _ = O.moe_forward(host, shape.top_k, shape.gate, True, routing=r)
+    out = layer.out.double().cpu().numpy()
+    assert np.all(np.isfinite(out))
+    if on or shape.n_shared:
+        assert P.rel_err(out, ref) <= P.OUT_TOL_BF16
+    else:
+        assert np.all(out == 0)
+    dout_h = I.round_to_bf16(np.random.default_rng(6).standard_normal(
+        (T, shape.d_model)).astype(np.float32))
+    grads = layer.backward(to_device(dout_h, torch.bfloat16, "cuda"))
+    assert B.moe_device_status(layer.bws) == (B.MOE_OK, 0)
+    assert all(torch.isfinite(v).all() for v in grads.values())
+    used = torch.from_numpy(np.isin(np.arange(shape.n_experts), idx)).cuda()
+    for key in ("dw1", "dw3", "dw2"):
+        assert torch.all(grads[key][~used] == 0)
+    if not on:
+        assert torch.all(grads["dw_router"] == 0)
+    if on:
+        gr = O.moe_backward(host, shape.top_k, shape.gate, bool(shape.norm_topk_prob), dout_h,
+                            routing=r)
+        for key in ("dw1", "dw3", "dw2"):
+            assert P.rel_err(grads[key].float().cpu().numpy(), gr[key]) <= 3e-2, key
+    upd = layer.orthogonalize(grads)
+    assert all(torch.isfinite(u).all() for u in upd.values())
+
+
+def test_layer_update_of_no_experts():
+    """An empty stack of gradients among others."""
+    layer = _layer("softmax")[2]
+    g = {"dw1": torch.empty(0, 300, 320, device="cuda"), "dw_router": torch.eye(40, device="cuda")}
+    out = layer.orthogonalize(g)
+    assert out["dw1"].shape == (0, 300, 320)
+    assert _ortho_err(out["dw_router"][None], g["dw_router"][None]) <= 100 * 2.0 ** -22 + 5e-6
