@@ -437,10 +437,9 @@ route_kernel(const RouteShape a, const L* __restrict__ logits, const float* __re
         } else {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const float key = v[c] + bv[c];
-            // NaN, +inf, or two finite terms whose sum leaves fp32's range
-            odd = odd || !(v[c] <= 1e30f) || (key == ninf && v[c] > ninf && bv[c] > ninf);
-            v[c] = v[c] > ninf ? key : ninf;
+            odd = odd || !(v[c] <= 1e30f);        // NaN or +inf
+            // rounded towards zero, two finite terms make a finite key
+            v[c] = v[c] > ninf ? __fadd_rz(v[c], bv[c]) : ninf;
           }
         }
       } else {
@@ -459,7 +458,7 @@ route_kernel(const RouteShape a, const L* __restrict__ logits, const float* __re
   float* mykeys = keys + tok * ROW;
   // A score's fp32 error: 2.5e-7 of a sigmoid; of a softmax, whose largest
   // term is row_inv, 9e-7 row_inv (the exponential 4e-7, the divisor 5e-7).  The
-  // sum with the bias rounds once more, 2^-24 of the key.
+  // sum with the bias rounds once more, 2^-24 of the key (2^-23 of a logit's).
   const float key_err = !by_score ? 0.f : a.gate == 0 ? 9e-7f * row_inv : 2.5e-7f;
   const int per = a.per;
   const bool limited = a.topk_group < a.groups;
@@ -506,14 +505,14 @@ route_kernel(const RouteShape a, const L* __restrict__ logits, const float* __re
           }
         }
       } else if (biased || two) {
-        if (two) sc = m1 + m2;
-        err = 2.f * key_err + 1.5e-7f * (fabsf(m1) + (two ? fabsf(m2) : 0.f));
+        // Beyond fp32's range a score is its lowest number, or inf, with a finite
+        // error: in order, or within its error of the border.  A key may have
+        // been cut to the lowest number already, in front of a large first one.
+        if (two) sc = fmaxf(m1 + m2, -FLT_MAX);
+        err = 2.f * key_err + (by_score ? 1.5e-7f : 2e-7f) * (fabsf(m1) + (two ? fabsf(m2) : 0.f));
+        err = m2 == -FLT_MAX && !by_score ? FLT_MAX : fminf(err, FLT_MAX);
       }
-      // A group with an eligible expert keeps a finite score and error, in the
-      // scores' order: what leaves fp32's range (a bias of +inf, sums of large
-      // ones) then lies within its error of the border, or clear of it.
-      if (m1 > ninf) sc = fminf(fmaxf(sc, -FLT_MAX), FLT_MAX);
-      picks[g] = make_int2(__float_as_int(fminf(err, FLT_MAX)), __float_as_int(sc));
+      picks[g] = make_int2(__float_as_int(err), __float_as_int(sc));
     }
     __syncwarp();
     use = 0;
@@ -562,7 +561,7 @@ route_kernel(const RouteShape a, const L* __restrict__ logits, const float* __re
               a, logits + static_cast<size_t>(t0 + r) * a.ld, bias, lane,
               __shfl_sync(kFull, lo, 8 * r), __shfl_sync(kFull, hi, 8 * r),
               picks + (r - tok) * kPickRow);
-          if (tok == r) use = u;
+          if (tok == r && __popc(u) == a.topk_group) use = u;   // as many as are read below
         }
       }
     }
@@ -584,7 +583,6 @@ route_kernel(const RouteShape a, const L* __restrict__ logits, const float* __re
   // --------------------------------------------------------------- 3 top-k
   const bool alive = on && ((slow >> (8 * tok)) & 0xffu) == 0u;
   const int total = limited && whole ? a.topk_group * per : a.E;   // experts to choose from
-  const int listed = limited && whole ? __popc(use) * per : a.E;   // the same
   const int nbr = (total + 31) >> 5;               // blocks of 4 of a lane
   // The lane's blocks: where they lie in the token's keys, and their keys in
   // descending order (a block that is not there holds none).
@@ -595,7 +593,7 @@ route_kernel(const RouteShape a, const L* __restrict__ logits, const float* __re
     const int p = 4 * (nbr * sub + i);
     base[i] = 0;
     float4 q = make_float4(ninf, ninf, ninf, ninf);
-    if (alive && i < nbr && p < total && p < listed) {
+    if (alive && i < nbr && p < total) {
       int e = p;
       if (limited && whole) {
         const int gi = static_cast<int>((p + 0.5f) * inv_per);
@@ -676,7 +674,8 @@ route_kernel(const RouteShape a, const L* __restrict__ logits, const float* __re
     // the logits: distinct ones have distinct fp64 scores, but next to zero
     // (below 1e-15 apart) and below `floor`, where the scores leave fp64's range.
     auto margin = [&](float key) {
-      return biased ? 2.f * key_err + 2e-7f * (fabsf(key) + 1e-3f) : 1e-12f;
+      return !biased ? 1e-12f
+                     : 2.f * key_err + (by_score ? 2e-7f : 2.6e-7f) * (fabsf(key) + 1e-3f);
     };
     const float floor = biased ? ninf : a.gate == 0 ? row_m - 700.f : -700.f;
     // equal inputs make equal keys: an exact tie, ordered by id as it should be
@@ -684,22 +683,21 @@ route_kernel(const RouteShape a, const L* __restrict__ logits, const float* __re
       return to_f32<L>(row[e]) == to_f32<L>(row[f]) && bias[e] == bias[f];
     };
     bool near = false;   // two neighbours of the chosen ones
-    bool huge = false;   // keys of +inf, whose gaps and margins say nothing
     bool edge = false;   // the last of them and the best one left out
     for (int j = sub; j + 1 < count; j += 8) {
       const int2 p = picks[j], n = picks[j + 1];
       const float best = __int_as_float(p.y), gap = best - __int_as_float(n.y);
       const bool c = !(gap > margin(best)) || best < floor;
-      if (best > FLT_MAX)
-        huge = true;
-      else if (j + 1 == a.k)
+      if (j + 1 == a.k)
         edge = c && (biased || fabsf(best) < 1e-6f || best < floor);
       else if (c)
         near = near || (biased ? !same(expert_at(p.x), expert_at(n.x)) : gap > 0.f);
     }
-    slow |= __ballot_sync(kFull, huge);
     if (__any_sync(kFull, near || edge)) {
       moved = true;
+      // keys of +inf, whose gaps and margins say nothing (and count as close)
+      slow |= __ballot_sync(kFull, count > 0 && __int_as_float(picks[0].y) > FLT_MAX);
+      if ((slow >> (8 * tok)) & 0xffu) near = edge = false;
       const unsigned edges = __ballot_sync(kFull, edge);
       bool open = ((edges >> (8 * tok)) & 0xffu) != 0u;
       unsigned fix = __ballot_sync(kFull, near), again = 0;
