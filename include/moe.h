@@ -182,7 +182,8 @@ moe_status moe_router_topk_opts(const moe_config* cfg, const void* x, const void
  *   w = scale s / (sum of the chosen s + 1e-9)  or  scale s
  *     (cfg->norm_topk_prob)
  * Equal scores or keys go to the lower id.  The selection is the one that
- * keys in fp64 give; weights are fp32.  Where fewer than top_k experts are
+ * keys in fp64 give (up to their own rounding; infinite biases, and sums that
+ * only fp64 holds, included); weights are fp32.  Where fewer than top_k experts are
  * eligible the remaining entries are id -1, weight 0 (moe_permute skips such
  * pairs and reports them as MOE_ERR_DATA, moe_combine adds nothing for them). */
 typedef struct {
@@ -467,7 +468,9 @@ moe_status moe_backward(const moe_config* cfg, const void* x, const void* w_rout
                         void* bws, size_t bws_bytes, void* stream);
 
 /* moe_forward with the router replaced by moe_route_groups on the layer's
- * logits (bf16 layers: the tensor cores' fp32 logits of moe_router_logits;
+ * logits (bf16 layers: the tensor cores' fp32 logits of moe_router_logits,
+ * taken as they are: near ties within their error, 5e-6, are not decided on
+ * exact logits as moe_forward's are;
  * fp32 layers: the fp64 sums of moe_router_topk's logits).  Arguments as
  * there; groups->logits_dtype must be MOE_F32.  token_mask [T] bytes or NULL:
  * a token with 0 (padding) goes to no expert, its out is the shared expert's
@@ -506,10 +509,10 @@ moe_status moe_backward_grouped(const moe_config* cfg, const moe_group_opts* gro
  * (the usual one: up to 5 steps; (2, -1.5, 0.5) or (3, -3.2, 1.2): any).
  * Errors relative to the exact iterate (2-norm of the whole matrix), before the
  * rounding to dtype_out, with the usual polynomial:
- *   22 bits  1e-6 to 2e-5 at 5 steps, up to 6e-5 at 6 and 4e-4 at 9.  Directions
+ *   22 bits  1e-6 to 3e-5 at 5 steps, up to 8e-5 at 6 and 4e-4 at 9.  Directions
  *            whose singular value is below about 1e-7 of the norm are noise,
  *            which grows a-fold per step as they do.
- *   11 bits  1e-3 to 3e-3 at 5 steps, less at fewer; up to 1.2e-2 where equal
+ *   11 bits  mostly 1e-3 to 2e-3 at 5 steps, up to 3e-3; up to 1.2e-2 where equal
  *            singular values meet sparse singular vectors (a scaled identity),
  *            whose roundings do not average out. */
 typedef struct {

@@ -16,12 +16,12 @@
 // nothing overflows, and the small elements of early iterates stay out of
 // fp16's subnormals); products accumulate in fp32.  Each value v is kept as
 // hi = fp16(v) and, where it counts, lo = fp16(v - hi), 22 bits together.
-//   TERMS = 3  (fp32 results, and bf16 ones of more steps) every product is hi lo + lo hi + hi hi and all
-//              of X, A, B are pairs.  The tensor cores' accumulator does not
-//              round to nearest, and its error grows with the inner
-//              dimension (1.7e-5 of the result at n = 2048), so it takes 256
-//              of it at a time and the epilogue adds those sums in fp32
-//              registers: errors near fp32's own.
+//   TERMS = 3  (fp32 results, and bf16 ones of more steps) every product is
+//              hi lo + lo hi + hi hi and all of X, A, B are pairs.  The
+//              tensor cores' accumulator does not round to nearest, and its
+//              error grows with the inner dimension (1.7e-5 of the result at
+//              n = 2048), so it takes 256 of it at a time and the epilogue
+//              adds those sums in fp32 registers: errors near fp32's own.
 //   TERMS = 1  (bf16 results) products of the hi planes alone, A and B
 //              without lo.  X keeps its lo plane for the a X term, except in
 //              the last step: the directions whose singular values are still
@@ -823,8 +823,9 @@ ns_gemm_kernel(const __grid_constant__ NsMaps maps, const NsArgs args) {
 //   poly    B = b A + c A A, by every CTA for itself, in A's place
 //   apply   X = a X + B X on its own columns, in place
 // What bounds it is latency: the products of one tile (24 with three terms, 8
-// with one, at 90 cycles), their epilogues' conversions, four block barriers and
-// three cluster barriers a step with their exchanges ([128, 128] fp32 39.5 us;
+// with one, at 90 cycles), their epilogues' conversions, four block barriers a step,
+// and two cluster barriers with their exchanges (four where rows are received in
+// A's place; [128, 128] fp32 39.5 us;
 // [100, 192] 46.7 us, bf16 31.1); 17 launches of the tiled kernel, 4 us each with
 // all their loads and stores, become one.
 constexpr int CL_ROWS = 128;
@@ -1617,7 +1618,9 @@ OrthoLayout ortho_layout(const OrthoShape& s) {
 
 // CTAs per cluster of the one-launch kernel, 0 where it does not apply.  Up to
 // four boxes stay in one CTA, which needs no exchange ([100, 192] bf16 31.1 us,
-// on two CTAs 38.8; fp32 of 256 columns 54.3, on four 51.2).  Above, two boxes a
+// on two CTAs 38.8), fp32 results as well, although one matrix of 256 columns would
+// gain a little (54.3 us, on four CTAs 51.2): it leaves the other SMs to a batch.
+// Above, two boxes a
 // CTA while every matrix has its cluster at once ([100, 512] bf16 41 us on four
 // CTAs, 51 on two; [100, 1024] 45 on eight, 52 on four), else four: the 16th
 // cluster of eight waits for another to end (16 of [100, 1024] bf16: 91 us on

@@ -19,10 +19,10 @@
 //
 // Bound by the selection's instructions for many tokens: 4 tokens per warp, 8
 // lanes each, so that the cross-lane steps of the top-k serve four tokens at a
-// time.  [131072, 256] fp32, 8 groups of which 4, top-8: 74 us, 1.8 TB/s of
+// time.  [131072, 256] fp32, 8 groups of which 4, top-8: 76 us, 1.8 TB/s of
 // logits, about 1950 instructions a warp (of 82 us with blocks of four warps,
 // the rounds of the top-k took 25, the groups 18, the keys 12, the margins 1).
-// [16384, 128]: 9.7 us.  One token: 4 us, of which the launch is half.
+// [16384, 128]: 9.8 us.  One token: 4 us, of which the launch is half.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
