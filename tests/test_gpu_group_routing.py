@@ -1030,3 +1030,22 @@ def test_layer_update_of_no_experts():
     out = layer.orthogonalize(g)
     assert out["dw1"].shape == (0, 300, 320)
     assert _ortho_err(out["dw_router"][None], g["dw_router"][None]) <= 100 * 2.0 ** -22 + 5e-6
+
+
+@pytest.mark.parametrize("shape", [(20, 700, 700), (40, 400, 805), (6, 805, 400), (64, 250, 287),
+                                   (24, 768, 2048), (1, 512, 2048), (2, 3000, 140),
+                                   (150, 100, 250), (12, 90, 1000), (1, 120, 4096)], ids=str)
+def test_orthogonalize_bf16_of_six_steps_in_batches(shape):
+    """bf16 results of three-term products on every tile shape and cluster width:
+    the fp32 results' error (1e-4 at six steps) and the rounding, 2^-8 at most."""
+    gen = torch.Generator(device="cuda").manual_seed(sum(shape))
+    g = torch.randn(*shape, generator=gen, device="cuda").to(torch.bfloat16)
+    out, ws = _ortho(g, torch.bfloat16, steps=6)
+    assert B.moe_device_status(ws) == (B.MOE_OK, 0)
+    ref = _ref64(g, steps=6)
+    err = torch.linalg.vector_norm(out.double() - ref, dim=(1, 2)) / \
+        torch.linalg.vector_norm(ref, dim=(1, 2))
+    assert err.max().item() <= 2.0 ** -8 + 1e-4
+    # and they are the fp32 results, rounded
+    full, _ = _ortho(g, torch.float32, steps=6)
+    assert torch.equal(out, full.to(torch.bfloat16))
